@@ -348,6 +348,160 @@ SSD_API ssd_status ssd_decode_window_flush(const ssd_dims *dims, ssd_dtype dtype
                                            float *state, const void *win_x, const float *win_dt,
                                            const void *win_B, const float *A, ssd_stream_t stream);
 
+/*
+ * The gated linear recurrence: a second mixer with one state value per channel, scanned
+ * over the sequence ("Engineering Hybrid State-Space Models" section 2: the diagonal
+ * recurrence h_t = Abar_t h_{t-1} + Bbar_t x_t, here with one learned decay per channel
+ * and two input-dependent gates).  Per batch row and channel d:
+ *
+ *     L_t = A_d * sigmoid(r_t)                      the log decay; A_d < 0
+ *     a_t = exp(L_t)
+ *     h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(i_t) * x_t
+ *
+ *   x, r, i   [batch, seqlen, dim] in the call's dtype: the input and the logits of the
+ *             recurrence and input gates.  Consecutive tokens are row_stride elements
+ *             apart (>= dim), batch rows seqlen * row_stride, the same for all three, so
+ *             they may be column slices of one projection's output.
+ *   A         [dim] fp32, finite and <= 0 (not checked: device data)
+ *   h         [batch, seqlen, dim] contiguous, in the call's dtype
+ *   states    [batch, dim] fp32
+ *
+ * fp32 arithmetic for both dtypes; bf16 outputs are rounded to nearest even.  1 - a^2 is
+ * formed from expm1(L), so decays close to 1 lose nothing.  Arrays need only the
+ * alignment of their elements; the wide-load path is taken when x, r, i, h (and their
+ * gradients) are 16-byte aligned and dim and the strides are multiples of 16 bytes.
+ */
+typedef struct {
+  int64_t batch;       /* >= 0                                                           */
+  int64_t seqlen;      /* >= 0 (ignored by ssd_glr_decode_step: one token)               */
+  int64_t dim;         /* >= 1: channels                                                 */
+  int64_t row_stride;  /* >= dim: elements between consecutive tokens of x, r and i      */
+  int64_t grad_stride; /* >= dim: the same of dx, dr and di (read by ssd_glr_backward only) */
+} ssd_glr_dims;
+
+/*
+ * The recurrence over whole sequences.  initial_state is h_{-1} (NULL: zero); final_state
+ * receives h_{seqlen-1} in fp32 (initial_state, or zero, when seqlen == 0) and may be
+ * initial_state itself (updated in place).  Pieces of a prompt continue from one another's
+ * final_state.  Errors: SSD_ERR_INVALID_ARG for NULL dims, negative sizes, dim < 1, a
+ * stride below dim, NULL or misaligned non-empty arrays, and batch * ceil(dim / 64) above
+ * 2^28 (the launch grid); SSD_ERR_CUDA if a launch fails.
+ */
+SSD_API ssd_status ssd_glr_prefill(const ssd_glr_dims *dims, ssd_dtype dtype, const void *x, const void *r,
+                                   const void *i, const float *A, const float *initial_state, void *h,
+                                   float *final_state, ssd_stream_t stream);
+
+/*
+ * One token of every sequence: x, r, i [batch, dim] (rows row_stride apart), h [batch, dim]
+ * contiguous; `state` is read as h_{t-1} and overwritten with h_t.  dims->seqlen is
+ * ignored.  Errors as ssd_glr_prefill.
+ */
+SSD_API ssd_status ssd_glr_decode_step(const ssd_glr_dims *dims, ssd_dtype dtype, float *state, const void *x,
+                                       const void *r, const void *i, const float *A, void *h, ssd_stream_t stream);
+
+/*
+ * Gradients of ssd_glr_prefill.  x, r, i, A and initial_state are its inputs and h its
+ * output; dh [batch, seqlen, dim] (contiguous, the call's dtype) is the gradient of h and
+ * dfinal_state (fp32, NULL: zero) that of final_state.  With c_seqlen = dfinal_state:
+ *
+ *     g_t = dh_t + c_{t+1};   c_t = a_t g_t;   dinitial_state = c_0
+ *     dx_t = g_t beta_t si_t;   di_t = dx_t x_t (1 - si_t)          beta = sqrt(1 - a^2), si = sigmoid(i)
+ *     dL_t = g_t (a_t h_{t-1} - a_t^2 / beta_t si_t x_t);   dr_t = dL_t L_t (1 - sr_t);   dA = sum dL_t sr_t
+ *
+ * dx, dr, di [batch, seqlen, dim] in the call's dtype, rows grad_stride apart (they may be
+ * column slices of one array); dA [dim] fp32, summed over batch and tokens in a fixed
+ * order; dinitial_state [batch, dim] fp32, or NULL; it may be dfinal_state.  Where a decay
+ * is exactly 1 (A_d = 0) the one-sided slope of sqrt(1 - a^2) is infinite and its term is
+ * taken as 0.  workspace: ssd_glr_backward_workspace_size() bytes of device scratch, 16-byte
+ * aligned; calls that share one must be ordered.  Errors as ssd_glr_prefill, plus
+ * SSD_ERR_WORKSPACE for a missing, misaligned or short workspace.
+ */
+SSD_API size_t ssd_glr_backward_workspace_size(const ssd_glr_dims *dims, ssd_dtype dtype);
+SSD_API ssd_status ssd_glr_backward(const ssd_glr_dims *dims, ssd_dtype dtype, const void *x, const void *r,
+                                    const void *i, const float *A, const float *initial_state, const void *h,
+                                    const void *dh, const float *dfinal_state, void *dx, void *dr, void *di,
+                                    float *dA, float *dinitial_state, void *workspace, size_t workspace_bytes,
+                                    ssd_stream_t stream);
+
+/*
+ * The norms before and after a mixer (ssd_prefill, ssd_decode_step, ssd_glr_*), each with
+ * its gradient.  Rows are tokens, whatever batch they come from: a prefill passes
+ * batch * seqlen rows, a decode step batch rows.  Statistics and arithmetic in fp32; each
+ * output is rounded once, to nearest even.  Arrays are row-major and contiguous except the
+ * gate z and its gradient, whose rows are gate_stride and dgate_stride elements apart (a
+ * slice of the block's input projection).  Arrays need only the alignment of their
+ * elements; 16-byte aligned arrays whose rows and groups are multiples of 16 bytes take the
+ * wide-load path.  weight, scale, dweight and dscale are fp32 [dim].
+ */
+typedef struct {
+  int64_t rows;         /* >= 0                                                               */
+  int64_t dim;          /* >= 1, multiple of ngroups                                          */
+  int64_t ngroups;      /* >= 1: a statistic for each dim / ngroups channels (gated norm only) */
+  int64_t gate_stride;  /* >= dim: elements between rows of z (gated norm only)               */
+  int64_t dgate_stride; /* >= dim: the same of dz (ssd_gated_norm_backward only)              */
+} ssd_norm_dims;
+
+/*
+ * Before a block: the residual stream takes in the last block's output, scaled per channel,
+ * and is normed for the next one.
+ *
+ *     s = residual + scale * x            (residual NULL: 0; scale NULL: 1)
+ *     residual_out = s                    (NULL: not written)
+ *     out = s / sqrt(mean(s^2) + eps) * weight
+ *
+ * x and out in `dtype`, residual and residual_out in `residual_dtype`: the same or fp32
+ * (otherwise SSD_ERR_UNSUPPORTED).  residual_out may be residual (updated in place); out is
+ * formed from the unrounded s.  Errors: SSD_ERR_INVALID_ARG for NULL dims, bad sizes (rows *
+ * ngroups above 2^31 - 1 among them) or types, eps not positive and finite, NULL or
+ * misaligned non-empty arrays.
+ */
+SSD_API ssd_status ssd_residual_norm(const ssd_norm_dims *dims, ssd_dtype dtype, ssd_dtype residual_dtype,
+                                     const void *x, const float *scale, const void *residual, const float *weight,
+                                     float eps, void *residual_out, void *out, ssd_stream_t stream);
+
+/*
+ * Its gradient, from residual_out as the forward wrote it (`s` here), dout (the gradient of
+ * out, in dtype) and dresidual_out (that of residual_out, in residual_dtype; NULL: zero):
+ *
+ *     n = s / sqrt(mean(s^2) + eps);   ds = (w dout - n mean(w dout n)) / sqrt(...) + dresidual_out
+ *     dresidual = ds;   dx = scale * ds;   dweight = sum over rows of dout n;   dscale = sum of ds x
+ *
+ * dx, dresidual, dweight and dscale may each be NULL (not wanted); x is read only for
+ * dscale.  dresidual may be dresidual_out.  The sums over rows go through per-CTA partial
+ * sums in a fixed order; workspace as ssd_glr_backward's, of
+ * ssd_norm_backward_workspace_size() bytes.
+ */
+SSD_API size_t ssd_norm_backward_workspace_size(const ssd_norm_dims *dims);
+SSD_API ssd_status ssd_residual_norm_backward(const ssd_norm_dims *dims, ssd_dtype dtype, ssd_dtype residual_dtype,
+                                              const void *x, const float *scale, const void *s, const float *weight,
+                                              float eps, const void *dout, const void *dresidual_out, void *dx,
+                                              void *dresidual, float *dweight, float *dscale, void *workspace,
+                                              size_t workspace_bytes, ssd_stream_t stream);
+
+/*
+ * After a mixer: its output y meets the gate z, silu(z) = z sigmoid(z), and the norm, whose
+ * statistics are taken over each of ngroups runs of dim / ngroups channels.
+ *
+ *     gate_first != 0:  v = y silu(z);  out = v / sqrt(mean(v^2) + eps) * weight
+ *     gate_first == 0:  out = y / sqrt(mean(y^2) + eps) * weight * silu(z)
+ *
+ * z and out in `dtype`, y in `y_dtype`: the same or fp32 (ssd_prefill writes y in fp32;
+ * otherwise SSD_ERR_UNSUPPORTED).  out may be y or z where type and stride agree (each
+ * element is read before it is written).  Errors as ssd_residual_norm.
+ */
+SSD_API ssd_status ssd_gated_norm(const ssd_norm_dims *dims, ssd_dtype dtype, ssd_dtype y_dtype, int gate_first,
+                                  const void *y, const void *z, const float *weight, float eps, void *out,
+                                  ssd_stream_t stream);
+
+/*
+ * Its gradient from y, z and dout (dtype): dy (y_dtype), dz (dtype, rows dgate_stride apart)
+ * and dweight, each of which may be NULL.  Workspace as ssd_residual_norm_backward.
+ */
+SSD_API ssd_status ssd_gated_norm_backward(const ssd_norm_dims *dims, ssd_dtype dtype, ssd_dtype y_dtype,
+                                           int gate_first, const void *y, const void *z, const float *weight,
+                                           float eps, const void *dout, void *dy, void *dz, float *dweight,
+                                           void *workspace, size_t workspace_bytes, ssd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,3 +10,4 @@ from .oracle import (  # noqa: F401
     default_threads,
 )
 from .frontend import frontend, causal_conv, softplus, silu  # noqa: F401,E402
+from . import block  # noqa: F401,E402

@@ -53,4 +53,49 @@ template <typename T>
 cudaError_t launch_decode_window_flush(float *state, const T *win_x, const float *win_dt, const T *win_B, int W,
                                        int count, const float *A, const Dims &d, cudaStream_t st);
 
+// Sizes of a gated linear recurrence (glr.cu): strides in elements.
+struct GlrDims {
+  int64_t b, L, D;
+  int64_t row;   // between consecutive tokens of x, r, i
+  int64_t grad;  // between consecutive tokens of dx, dr, di
+};
+
+// glr.cu
+template <typename T>
+cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h,
+                               float *final_state, const GlrDims &d, cudaStream_t st);
+template <typename T>
+cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T *i, const float *A, T *h,
+                                   const GlrDims &d, cudaStream_t st);
+// floats of scratch: the partial sums of dA
+size_t glr_backward_floats(const GlrDims &d);
+template <typename T>
+cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float *A, const float *init, const T *h,
+                                const T *dh, const float *dfinal, T *dx, T *dr, T *di, float *dA, float *dinit,
+                                float *part, const GlrDims &d, cudaStream_t st);
+
+// Sizes of the norms (norm.cu); the residual norm has one group.
+struct NormDims {
+  int64_t rows, D, G;
+  int64_t gate, dgate;  // elements between rows of z and of dz
+};
+
+// norm.cu.  TX: x, z, out, dout; TR: residual stream or y.
+template <typename TX, typename TR>
+cudaError_t launch_residual_norm(const TX *x, const float *scale, const TR *res, const float *w, float eps,
+                                 TR *res_out, TX *out, const NormDims &d, cudaStream_t st);
+// floats of scratch: the partial sums of two vectors of dim
+size_t norm_backward_floats(const NormDims &d);
+template <typename TX, typename TR>
+cudaError_t launch_residual_norm_backward(const TX *x, const float *scale, const TR *s, const float *w, float eps,
+                                          const TX *dout, const TR *dres_out, TX *dx, TR *dres, float *dw,
+                                          float *dscale, float *part, const NormDims &d, cudaStream_t st);
+template <typename TX, typename TR>
+cudaError_t launch_gated_norm(bool gate_first, const TR *y, const TX *z, const float *w, float eps, TX *out,
+                              const NormDims &d, cudaStream_t st);
+template <typename TX, typename TR>
+cudaError_t launch_gated_norm_backward(bool gate_first, const TR *y, const TX *z, const float *w, float eps,
+                                       const TX *dout, TR *dy, TX *dz, float *dw, float *part, const NormDims &d,
+                                       cudaStream_t st);
+
 }  // namespace ssd

@@ -6,18 +6,20 @@
 #include <string.h>
 
 #include "ssd.h"
+#include "api_internal.h"
 #include "kernels.h"
 
 namespace {
 
+using ssd::aligned;
+using ssd::check_ptr;
+using ssd::cuda_status;
 using ssd::Dims;
 
 constexpr int kVersion = 100;  // 0.1.0
 constexpr size_t kAlign = 256;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -49,12 +51,6 @@ ssd_status check_dims(const ssd_dims *dims, ssd_dtype dtype, bool prefill, Dims 
   d->G = (int)dims->ngroups;
   d->hpg = d->H / d->G;
   return SSD_OK;
-}
-
-// Every non-empty array must be non-NULL and aligned.
-bool check_ptr(const void *p, int64_t elems, size_t align) {
-  if (elems == 0) return true;
-  return p != nullptr && aligned(p, align);
 }
 
 enum class Path { kNone, kSimt, kTensorCore };
@@ -95,8 +91,6 @@ PrefillPlan plan_prefill(const Dims &d, ssd_dtype dtype, int Q) {
   }
   return pl;
 }
-
-ssd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
 // Records events[i] before kernel i (and events[k] after the last) when events != NULL.
 struct Marker {

@@ -30,13 +30,26 @@ class Dims(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64)]
 
 
+class GlrDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("dgate_stride", ctypes.c_int64)]
+
+
 # Every symbol include/ssd.h declares.
 EXPORTS = ("ssd_status_string", "ssd_version", "ssd_prefill_workspace_size",
            "ssd_prefill_kernel_launches", "ssd_prefill", "ssd_prefill_ex", "ssd_prefill_timed",
            "ssd_prefill_kernel_name", "ssd_prefill_device_status", "ssd_prefill_noalloc",
            "ssd_prefill_noalloc_max_workspace", "ssd_prefill_noalloc_device_status", "ssd_decode_step",
            "ssd_frontend", "ssd_decode_window_step", "ssd_decode_window_flush", "ssd_wait_selftest",
-           "ssd_prefill_host_buffer_size", "ssd_prefill_host")
+           "ssd_prefill_host_buffer_size", "ssd_prefill_host", "ssd_glr_prefill", "ssd_glr_decode_step",
+           "ssd_glr_backward_workspace_size", "ssd_glr_backward", "ssd_residual_norm",
+           "ssd_norm_backward_workspace_size", "ssd_residual_norm_backward", "ssd_gated_norm",
+           "ssd_gated_norm_backward")
 
 
 def _load():
@@ -85,6 +98,20 @@ def _load():
     lib.ssd_decode_window_step.restype = ci
     lib.ssd_decode_window_flush.argtypes = [dp, ci, ci, ci, fp, vp, fp, vp, fp, vp]
     lib.ssd_decode_window_flush.restype = ci
+    gp, np_, f32 = ctypes.POINTER(GlrDims), ctypes.POINTER(NormDims), ctypes.c_float
+    for name, args in (("ssd_glr_prefill", [gp, ci] + [vp] * 8),
+                       ("ssd_glr_decode_step", [gp, ci] + [vp] * 7),
+                       ("ssd_glr_backward", [gp, ci] + [vp] * 14 + [sz, vp]),
+                       ("ssd_residual_norm", [np_, ci, ci, vp, vp, vp, vp, f32, vp, vp, vp]),
+                       ("ssd_residual_norm_backward", [np_, ci, ci, vp, vp, vp, vp, f32] + [vp] * 7 + [sz, vp]),
+                       ("ssd_gated_norm", [np_, ci, ci, ci, vp, vp, vp, f32, vp, vp]),
+                       ("ssd_gated_norm_backward", [np_, ci, ci, ci, vp, vp, vp, f32] + [vp] * 5 + [sz, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ci
+    lib.ssd_glr_backward_workspace_size.argtypes = [gp, ci]
+    lib.ssd_glr_backward_workspace_size.restype = sz
+    lib.ssd_norm_backward_workspace_size.argtypes = [np_]
+    lib.ssd_norm_backward_workspace_size.restype = sz
     return lib
 
 
@@ -432,3 +459,293 @@ def wait_selftest(workspace, limit_ns: int = 1_000_000, expire: bool = True, str
     if st != OK:
         raise SSDError(st, "ssd_wait_selftest")
     return prefill_device_status(workspace, stream)
+
+
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"unsupported {name} dtype {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError("libssd runs on CUDA tensors only")
+    return t.device
+
+
+def _call(where: str, dev: torch.device, stream, args) -> None:
+    """fn(*args, stream) on the tensors' device, on `stream` or that device's current one."""
+    fn = getattr(lib, where)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    if st != OK:
+        raise SSDError(st, where)
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """Elements between consecutive rows of a [..., D] array whose rows may be slices of wider
+    ones: unit stride within a row, one stride from row to row over all leading axes."""
+    if t.device != device or t.dtype != dtype or t.shape != shape:
+        _check(t, name, shape, dtype, device)
+    D = shape[-1]
+    if t.is_contiguous():
+        return D
+    strides, row, n = t.stride(), None, 1
+    for k in range(len(shape) - 2, -1, -1):
+        if shape[k] == 1:
+            continue
+        if row is None:
+            row = strides[k]
+        elif strides[k] != row * n:
+            raise ValueError(f"{name} has strides {tuple(strides)}: its rows must be evenly spaced")
+        n *= shape[k]
+    row = D if row is None or n == 0 else row
+    if (D > 1 and strides[-1] != 1) or row < D:
+        raise ValueError(f"{name} has strides {tuple(strides)}: its rows must be contiguous and not overlap")
+    return row
+
+
+def _same_stride(tensors, shape, dtype, device) -> int:
+    rows = [_row_stride(t, name, shape, dtype, device) for name, t in tensors]
+    many = 1
+    for k in shape[:-1]:
+        many *= k
+    if many > 1 and any(r != rows[0] for r in rows):
+        raise ValueError(f"{', '.join(n for n, _ in tensors)} must have the same row stride, got {rows}")
+    return rows[0]
+
+
+def _workspace(workspace, need: int, dev):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream=None):
+    """ssd_glr_prefill: the gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with
+    a_t = exp(A sigmoid(r_t)), over x, r, i [b, L, D] (fp32 or bf16; they may be column slices of one array)
+    and A [D] fp32 (<= 0), from initial_state [b, D] fp32 (None: zero).  Returns (h [b, L, D] in x's dtype,
+    final_state [b, D] fp32); final_state may be initial_state."""
+    if x.dim() != 3:
+        raise ValueError("x, r and i must be [b,L,D]")
+    dev = _cuda(x, "x")
+    shape = x.shape
+    b, L, D = shape
+    row = _same_stride((("x", x), ("r", r), ("i", i)), shape, x.dtype, dev)
+    _check(A, "A", (D,), torch.float32, dev)
+    if initial_state is not None:
+        _check(initial_state, "initial_state", (b, D), torch.float32, dev)
+    if h is None:
+        h = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _check(h, "h", shape, x.dtype, dev)
+    if final_state is None:
+        final_state = torch.empty((b, D), dtype=torch.float32, device=dev)
+    else:
+        _check(final_state, "final_state", (b, D), torch.float32, dev)
+    dims = GlrDims(b, L, D, row, D)
+    _call("ssd_glr_prefill", dev, stream,
+          (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
+           _address(initial_state), h.data_ptr(), final_state.data_ptr()))
+    return h, final_state
+
+
+def glr_decode_step(state, x, r, i, A, h=None, stream=None) -> torch.Tensor:
+    """ssd_glr_decode_step: one token of every sequence.  Updates `state` [b, D] fp32 in place and returns h
+    [b, D]; x, r, i [b, D] as for glr_prefill (their rows may be slices)."""
+    if x.dim() != 2:
+        raise ValueError("x, r and i must be [b,D]")
+    dev = _cuda(x, "x")
+    shape = x.shape
+    b, D = shape
+    row = _same_stride((("x", x), ("r", r), ("i", i)), shape, x.dtype, dev)
+    _check(A, "A", (D,), torch.float32, dev)
+    _check(state, "state", (b, D), torch.float32, dev)
+    if h is None:
+        h = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _check(h, "h", shape, x.dtype, dev)
+    dims = GlrDims(b, 1, D, row, D)
+    _call("ssd_glr_decode_step", dev, stream,
+          (ctypes.byref(dims), _DTYPES[x.dtype], state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(),
+           A.data_ptr(), h.data_ptr()))
+    return h
+
+
+def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=None, dr=None, di=None, dA=None,
+                 dinitial_state=None, workspace=None, stream=None):
+    """ssd_glr_backward: gradients of glr_prefill from its inputs, its output h, and the gradients dh of h
+    and dfinal_state of the final state (None: zero).  Returns (dx, dr, di, dA, dinitial_state); dx, dr and di
+    given by the caller may be column slices of one array."""
+    if x.dim() != 3:
+        raise ValueError("x, r and i must be [b,L,D]")
+    dev = _cuda(x, "x")
+    shape = x.shape
+    b, L, D = shape
+    row = _same_stride((("x", x), ("r", r), ("i", i)), shape, x.dtype, dev)
+    _check(A, "A", (D,), torch.float32, dev)
+    _check(h, "h", shape, x.dtype, dev)
+    _check(dh, "dh", shape, x.dtype, dev)
+    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state),
+                    ("dinitial_state", dinitial_state)):
+        if t is not None:
+            _check(t, name, (b, D), torch.float32, dev)
+    dx = torch.empty(shape, dtype=x.dtype, device=dev) if dx is None else dx
+    dr = torch.empty(shape, dtype=x.dtype, device=dev) if dr is None else dr
+    di = torch.empty(shape, dtype=x.dtype, device=dev) if di is None else di
+    grad = _same_stride((("dx", dx), ("dr", dr), ("di", di)), shape, x.dtype, dev)
+    if dA is None:
+        dA = torch.empty(D, dtype=torch.float32, device=dev)
+    else:
+        _check(dA, "dA", (D,), torch.float32, dev)
+    if dinitial_state is None:
+        dinitial_state = torch.empty((b, D), dtype=torch.float32, device=dev)
+    dims = GlrDims(b, L, D, row, grad)
+    need = lib.ssd_glr_backward_workspace_size(ctypes.byref(dims), _DTYPES[x.dtype])
+    workspace, nbytes = _workspace(workspace, need, dev)
+    _call("ssd_glr_backward", dev, stream,
+          (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
+           _address(initial_state), h.data_ptr(), dh.data_ptr(), _address(dfinal_state), dx.data_ptr(),
+           dr.data_ptr(), di.data_ptr(), dA.data_ptr(), dinitial_state.data_ptr(), workspace.data_ptr(), nbytes))
+    return dx, dr, di, dA, dinitial_state
+
+
+def _norm_rows(t: torch.Tensor, name: str):
+    if t.dim() < 1:
+        raise ValueError(f"{name} must be [..., D]")
+    D = t.shape[-1]
+    if D < 1:
+        raise ValueError(f"{name} has no channels")
+    return t.numel() // D, D
+
+
+def residual_norm(x, weight, residual=None, scale=None, residual_dtype=None, eps: float = 1e-5, residual_out=None,
+                  out=None, stream=None):
+    """ssd_residual_norm, before a block: s = residual + scale * x (residual None: 0; scale None: 1), out =
+    s / sqrt(mean(s^2) + eps) * weight over the last axis.  x [..., D] fp32 or bf16; residual in x's dtype or
+    fp32; weight, scale [D] fp32.  Returns (out in x's dtype, s in residual_dtype: residual's, else x's);
+    residual_out may be residual."""
+    dev = _cuda(x, "x")
+    shape = x.shape
+    rows, D = _norm_rows(x, "x")
+    _check(x, "x", shape, x.dtype, dev)
+    if residual_dtype is None:
+        residual_dtype = residual.dtype if residual is not None else \
+            residual_out.dtype if residual_out is not None else x.dtype
+    if residual_dtype not in _DTYPES:
+        raise ValueError(f"unsupported residual dtype {residual_dtype}")
+    _check(weight, "weight", (D,), torch.float32, dev)
+    if scale is not None:
+        _check(scale, "scale", (D,), torch.float32, dev)
+    if residual is not None:
+        _check(residual, "residual", shape, residual_dtype, dev)
+    if residual_out is None:
+        residual_out = torch.empty(shape, dtype=residual_dtype, device=dev)
+    else:
+        _check(residual_out, "residual_out", shape, residual_dtype, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _check(out, "out", shape, x.dtype, dev)
+    dims = NormDims(rows, D, 1, D, D)
+    _call("ssd_residual_norm", dev, stream,
+          (ctypes.byref(dims), _DTYPES[x.dtype], _DTYPES[residual_dtype], x.data_ptr(), _address(scale),
+           _address(residual), weight.data_ptr(), eps, residual_out.data_ptr(), out.data_ptr()))
+    return out, residual_out
+
+
+def residual_norm_backward(dout, s, weight, x=None, scale=None, dresidual_out=None, eps: float = 1e-5, dx=None,
+                           dresidual=None, dweight=None, dscale=None, workspace=None, stream=None):
+    """ssd_residual_norm_backward: gradients of residual_norm from dout, the sum `s` it returned, and the
+    gradient dresidual_out of that sum (None: zero); x is needed with a scale.  Returns (dx, dresidual,
+    dweight, dscale), dscale None without a scale; dresidual may be dresidual_out."""
+    dev = _cuda(dout, "dout")
+    if s.dtype not in _DTYPES:
+        raise ValueError(f"unsupported s dtype {s.dtype}")
+    shape = dout.shape
+    rows, D = _norm_rows(dout, "dout")
+    _check(dout, "dout", shape, dout.dtype, dev)
+    _check(s, "s", shape, s.dtype, dev)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    if dresidual_out is not None:
+        _check(dresidual_out, "dresidual_out", shape, s.dtype, dev)
+    if scale is not None:
+        _check(scale, "scale", (D,), torch.float32, dev)
+        if x is None:
+            raise ValueError("the gradient of scale needs x")
+        _check(x, "x", shape, dout.dtype, dev)
+        dscale = torch.empty(D, dtype=torch.float32, device=dev) if dscale is None else dscale
+        _check(dscale, "dscale", (D,), torch.float32, dev)
+    elif dscale is not None:
+        raise ValueError("dscale without a scale")
+    dx = torch.empty(shape, dtype=dout.dtype, device=dev) if dx is None else dx
+    dresidual = torch.empty(shape, dtype=s.dtype, device=dev) if dresidual is None else dresidual
+    dweight = torch.empty(D, dtype=torch.float32, device=dev) if dweight is None else dweight
+    _check(dx, "dx", shape, dout.dtype, dev)
+    _check(dresidual, "dresidual", shape, s.dtype, dev)
+    _check(dweight, "dweight", (D,), torch.float32, dev)
+    dims = NormDims(rows, D, 1, D, D)
+    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), dev)
+    _call("ssd_residual_norm_backward", dev, stream,
+          (ctypes.byref(dims), _DTYPES[dout.dtype], _DTYPES[s.dtype], _address(x if scale is not None else None),
+           _address(scale), s.data_ptr(), weight.data_ptr(), eps, dout.data_ptr(), _address(dresidual_out),
+           dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(), _address(dscale), workspace.data_ptr(), nbytes))
+    return dx, dresidual, dweight, dscale
+
+
+def gated_norm(y, z, weight, ngroups: int = 1, gate_first: bool = True, eps: float = 1e-5, out=None,
+               stream=None) -> torch.Tensor:
+    """ssd_gated_norm, after a mixer: with silu(z) = z sigmoid(z) and the mean over each of ngroups runs of
+    channels, v / sqrt(mean(v^2) + eps) * weight for v = y silu(z) (gate_first), or the norm of y times
+    silu(z).  y [..., D] in z's dtype or fp32 (as ssd_prefill writes it; heads are flattened by the caller); z
+    fp32 or bf16, its rows may be slices of a projection's; weight [D] fp32.  Returns out in z's dtype."""
+    dev = _cuda(z, "z")
+    if y.dtype not in _DTYPES:
+        raise ValueError(f"unsupported y dtype {y.dtype}")
+    shape = y.shape
+    rows, D = _norm_rows(y, "y")
+    _check(y, "y", shape, y.dtype, dev)
+    gate = _row_stride(z, "z", shape, z.dtype, dev)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=z.dtype, device=dev)
+    else:
+        _check(out, "out", shape, z.dtype, dev)
+    dims = NormDims(rows, D, int(ngroups), gate, D)
+    _call("ssd_gated_norm", dev, stream,
+          (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
+           weight.data_ptr(), eps, out.data_ptr()))
+    return out
+
+
+def gated_norm_backward(dout, y, z, weight, ngroups: int = 1, gate_first: bool = True, eps: float = 1e-5, dy=None,
+                        dz=None, dweight=None, workspace=None, stream=None):
+    """ssd_gated_norm_backward: gradients of gated_norm from dout (z's dtype).  Returns (dy, dz, dweight); a
+    dz given by the caller may be a slice of the projection's gradient."""
+    dev = _cuda(z, "z")
+    if y.dtype not in _DTYPES:
+        raise ValueError(f"unsupported y dtype {y.dtype}")
+    shape = y.shape
+    rows, D = _norm_rows(y, "y")
+    _check(y, "y", shape, y.dtype, dev)
+    gate = _row_stride(z, "z", shape, z.dtype, dev)
+    _check(dout, "dout", shape, z.dtype, dev)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    dy = torch.empty(shape, dtype=y.dtype, device=dev) if dy is None else dy
+    dz = torch.empty(shape, dtype=z.dtype, device=dev) if dz is None else dz
+    dweight = torch.empty(D, dtype=torch.float32, device=dev) if dweight is None else dweight
+    _check(dy, "dy", shape, y.dtype, dev)
+    dgate = _row_stride(dz, "dz", shape, z.dtype, dev)
+    _check(dweight, "dweight", (D,), torch.float32, dev)
+    dims = NormDims(rows, D, int(ngroups), gate, dgate)
+    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), dev)
+    _call("ssd_gated_norm_backward", dev, stream,
+          (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
+           weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(),
+           workspace.data_ptr(), nbytes))
+    return dy, dz, dweight
