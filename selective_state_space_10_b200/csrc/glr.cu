@@ -3,6 +3,8 @@
 //   L_t = A sigmoid(r_t),  a_t = exp(L_t),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
 //
 // over whole sequences, for one token, and its gradients.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -73,24 +75,219 @@ __device__ __forceinline__ void gate(float x, float r, float i, float A, float &
   b = sqrt_approx(rest) * pick(i, sigmoid_small(i)) * x;
 }
 
-// One thread per (batch row, channel), walking the sequence.
-template <typename T>
-__global__ void __launch_bounds__(128) k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r,
-                                                     const T *__restrict__ i, const float *__restrict__ A,
-                                                     const float *init, T *__restrict__ h, float *final_state,
-                                                     GlrDims d, int blocks) {
-  const int64_t b = blockIdx.x / blocks, c = (int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x;
-  if (c >= d.D) return;
-  const float Ac = A[c];
-  float s = init != nullptr ? init[b * d.D + c] : 0.f;
-  for (int64_t t = 0; t < d.L; ++t) {
-    const int64_t at = (b * d.L + t) * d.row + c;
-    float a, v;
-    gate(to_f32(x[at]), to_f32(r[at]), to_f32(i[at]), Ac, a, v);
-    s = fmaf(a, s, v);
-    h[(b * d.L + t) * d.D + c] = from_f32<T>(s);
+// The scans.  A CTA takes 64 channels (two a lane) of one batch row and walks the sequence in
+// tiles of 64 tokens, 8 a warp.  Each warp copies its own tokens of the next tiles into
+// shared memory (two stages) while it forms the gates of this one, keeps its 8 decays and
+// input terms in registers, and publishes what they do to a state, h -> A h + H, as one
+// float4 a lane.  After a barrier a warp applies the warps before it to the carried state and
+// runs its 8 steps: every array is read and written once.  Where the channels alone leave
+// the GPU idle, a cluster of up to 8 CTAs shares a sequence, a tile each in turn: the CTAs'
+// own A h + H go to the ranks behind them through distributed shared memory.
+constexpr int kW = 8;          // warps
+constexpr int kT = 8;          // tokens a warp
+constexpr int kTile = kW * kT;
+constexpr int kCh = 64;        // channels a CTA
+constexpr int kMaxRanks = 8;
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// CW bytes global -> shared, zeros when !valid (nothing is read then)
+template <int CW>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool valid) {
+  const int n = valid ? CW : 0;
+  if constexpr (CW == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_async() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A warp's copy of rows t .. t + 7 (of those in [0, L)) of 64 channels from c0 on.  `base` is
+// the batch row's first element.  CW: bytes a copy (16 or 4), or 0 for element loads.
+template <typename T, int CW>
+__device__ __forceinline__ void fetch(T *dst, const T *base, int64_t t, int64_t L, int64_t stride, int64_t c0,
+                                      int64_t D, int lane) {
+  if constexpr (CW == 0) {
+#pragma unroll
+    for (int q = 0; q < kT * kCh / 32; ++q) {
+      const int row = q * 32 / kCh, c = q * 32 % kCh + lane;
+      const int64_t tt = t + row;
+      const bool valid = tt >= 0 && tt < L && c0 + c < D;
+      dst[row * kCh + c] = valid ? base[tt * stride + c0 + c] : T(0.f);
+    }
+  } else {
+    constexpr int E = CW / (int)sizeof(T), CPR = kCh / E, N = kT * CPR / 32;  // elements a copy, copies a row
+    const uint32_t to = smem_addr(dst) + lane * CW;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int row = CPR <= 32 ? q * (32 / CPR) + lane / CPR : q / (CPR / 32);
+      const int c = (CPR <= 32 ? lane % CPR : q % (CPR / 32) * 32 + lane) * E;
+      const int64_t tt = t + row;
+      const bool valid = tt >= 0 && tt < L && c0 + c < D;
+      copy_async<CW>(to + q * 32 * CW, valid ? base + tt * stride + c0 + c : base, valid);
+    }
   }
-  final_state[b * d.D + c] = s;
+}
+
+__device__ __forceinline__ float2 pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 pair(const __nv_bfloat16 *p) {
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// Two neighbouring channels out; kPair: the address is aligned for both and both exist.
+template <bool kPair, typename T>
+__device__ __forceinline__ void store2(T *p, float u, float v, int n) {
+  if constexpr (kPair) {
+    if (n < 2) return;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2 *>(p) = make_float2(u, v);
+    else
+      *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(u, v);
+  } else {
+    if (n > 0) p[0] = from_f32<T>(u);
+    if (n > 1) p[1] = from_f32<T>(v);
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// A barrier of the cluster: every write to distributed shared memory before it is seen after.
+__device__ __forceinline__ void sync_ranks() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void store_rank(void *p, uint32_t rank, float4 v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// State updates h -> A h + H of two channels {A0, H0, A1, H1}: `second` after `first`.
+__device__ __forceinline__ float4 then(float4 first, float4 second) {
+  return make_float4(first.x * second.x, fmaf(second.x, first.y, second.y), first.z * second.z,
+                     fmaf(second.z, first.w, second.w));
+}
+__device__ __forceinline__ float2 apply(float4 f, float2 h) {
+  return make_float2(fmaf(f.x, h.x, f.y), fmaf(f.z, h.y, f.w));
+}
+
+// What the warps and ranks of a scan tell one another, by parity of the tile.
+struct Links {
+  float4 warp[2][kW][32];
+  float4 rank[2][kMaxRanks][32];
+  float4 carry[2][32];  // x, y: the state entering the tile
+};
+
+// The state entering this warp's tokens, given its own update `mine`; all ranks call it once a tile.
+template <bool kCluster>
+__device__ __forceinline__ float2 enter(Links &l, int par, int warp, int lane, int rank, int ranks, float4 mine) {
+  l.warp[par][warp][lane] = mine;
+  __syncthreads();
+  float4 before = make_float4(1.f, 0.f, 1.f, 0.f);
+  for (int w = 0; w < warp; ++w) before = then(before, l.warp[par][w][lane]);
+  if constexpr (kCluster) {
+    if (warp == kW - 1) {
+      const float4 all = then(before, mine);
+      for (int k = rank + 1; k < ranks; ++k) store_rank(&l.rank[par][rank][lane], k, all);
+    }
+    sync_ranks();
+  }
+  const float4 c = l.carry[par][lane];
+  float2 h = make_float2(c.x, c.y);
+  if constexpr (kCluster)
+    for (int k = 0; k < rank; ++k) h = apply(l.rank[par][k][lane], h);
+  return apply(before, h);
+}
+// The state after the tile's last token, from the last warp of the last rank, for the next tile (not
+// after the last one: a rank may have left by then).
+template <bool kCluster>
+__device__ __forceinline__ void leave(Links &l, int par, int lane, int ranks, float2 h) {
+  const float4 v = make_float4(h.x, h.y, 0.f, 0.f);
+  if constexpr (kCluster)
+    for (int k = 0; k < ranks; ++k) store_rank(&l.carry[par ^ 1][lane], k, v);
+  else
+    l.carry[par ^ 1][lane] = v;
+}
+
+template <typename T, int N>
+struct ScanSmem {
+  T in[kW][2][N][kT][kCh];
+  Links links;
+};
+
+template <typename T, int CW, bool kCluster>
+__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 3 : 2)
+    k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
+                  const float *__restrict__ A, const float *init, T *__restrict__ h, float *final_state, GlrDims d,
+                  int blocks) {
+  extern __shared__ __align__(16) char raw[];
+  ScanSmem<T, 3> &sm = *reinterpret_cast<ScanSmem<T, 3> *>(raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = kCluster ? cluster_rank() : 0, ranks = kCluster ? cluster_size() : 1;
+  const int64_t blk = blockIdx.x / ranks, b = blk / blocks, c0 = blk % blocks * kCh, c = c0 + 2 * lane;
+  const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));  // channels of this lane
+  const float A0 = n > 0 ? A[c] : 0.f, A1 = n > 1 ? A[c + 1] : 0.f;
+  const T *const in[3] = {x + b * d.L * d.row, r + b * d.L * d.row, i + b * d.L * d.row};
+  const int64_t tiles = (d.L + kTile * ranks - 1) / (kTile * ranks);
+  auto first = [&](int64_t tile) { return (tile * ranks + rank) * kTile + warp * kT; };
+  auto load = [&](int64_t tile) {
+    if (tile < tiles) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        fetch<T, CW>(&sm.in[warp][tile & 1][k][0][0], in[k], first(tile), d.L, d.row, c0, d.D, lane);
+    }
+    commit_async();
+  };
+  load(0);
+  load(1);
+  if (warp == 0)
+    sm.links.carry[0][lane] = init != nullptr ? make_float4(n > 0 ? init[b * d.D + c] : 0.f,
+                                                            n > 1 ? init[b * d.D + c + 1] : 0.f, 0.f, 0.f)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (kCluster) sync_ranks();  // no rank writes to another that has not started
+  float2 s = make_float2(0.f, 0.f);
+  for (int64_t tile = 0; tile < tiles; ++tile) {
+    const int par = tile & 1;
+    const int64_t t = first(tile);
+    wait_async<1>();
+    __syncwarp();
+    float2 a[kT], v[kT];
+    float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kT; ++j) {
+      const float2 xj = pair(&sm.in[warp][par][0][j][2 * lane]), rj = pair(&sm.in[warp][par][1][j][2 * lane]),
+                   ij = pair(&sm.in[warp][par][2][j][2 * lane]);
+      gate(xj.x, rj.x, ij.x, A0, a[j].x, v[j].x);
+      gate(xj.y, rj.y, ij.y, A1, a[j].y, v[j].y);
+      if (t + j >= d.L) a[j] = make_float2(1.f, 1.f), v[j] = make_float2(0.f, 0.f);
+      all = then(all, make_float4(a[j].x, v[j].x, a[j].y, v[j].y));
+    }
+    __syncwarp();
+    load(tile + 2);
+    s = enter<kCluster>(sm.links, par, warp, lane, rank, ranks, all);
+    T *out = h + (b * d.L + t) * d.D + c;
+#pragma unroll
+    for (int j = 0; j < kT; ++j) {
+      s = make_float2(fmaf(a[j].x, s.x, v[j].x), fmaf(a[j].y, s.y, v[j].y));
+      if (t + j < d.L) store2<CW == 16>(out + j * d.D, s.x, s.y, n);
+    }
+    if (warp == kW - 1 && rank == ranks - 1 && tile + 1 < tiles) leave<kCluster>(sm.links, par, lane, ranks, s);
+  }
+  if (warp == kW - 1 && rank == ranks - 1) store2<false>(final_state + b * d.D + c, s.x, s.y, n);
 }
 
 template <typename T>
@@ -153,12 +350,46 @@ __global__ void __launch_bounds__(128) k_glr_sum(const float *__restrict__ part,
 
 }  // namespace
 
+bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// CTAs that share a sequence: as many as the GPU holds at once (`resident` an SM) and the
+// sequence has tiles for.
+int pick_ranks(int64_t ctas, int64_t L, int resident) {
+  const int64_t room = (int64_t)148 * resident / ctas, tiles = (L + kTile - 1) / kTile;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({room, tiles, kMaxRanks}));
+}
+
+template <typename... P, typename... V>
+cudaError_t launch_ranks(void (*f)(P...), int64_t ctas, int ranks, size_t smem, cudaStream_t st, V... v) {
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(ctas * ranks));
+  cfg.blockDim = dim3(kW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim = {(unsigned)ranks, 1, 1};
+  cfg.attrs = &at;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, v...);
+}
+
 template <typename T>
 cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h,
                                float *final_state, const GlrDims &d, cudaStream_t st) {
-  const int64_t blocks = (d.D + 127) / 128;
-  k_glr_prefill<T><<<(unsigned)(blocks * d.b), 128, 0, st>>>(x, r, i, A, init, h, final_state, d, (int)blocks);
-  return cudaGetLastError();
+  const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
+  constexpr int E = 16 / sizeof(T);
+  const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && d.D % E == 0 && d.row % E == 0;
+  const int ranks = pick_ranks(ctas, d.L, sizeof(T) == 2 ? 3 : 1);
+  auto run = [&](auto *one, auto *many) {
+    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, sizeof(ScanSmem<T, 3>), st, x, r, i, A, init, h,
+                        final_state, d, (int)blocks);
+  };
+  if (w16) return run(k_glr_prefill<T, 16, false>, k_glr_prefill<T, 16, true>);
+  constexpr int CW = sizeof(T) == 4 ? 4 : 0;
+  return run(k_glr_prefill<T, CW, false>, k_glr_prefill<T, CW, true>);
 }
 
 template <typename T>
