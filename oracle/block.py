@@ -70,7 +70,8 @@ def glr_backward(x, r, i, A, h, dh, h0=None, dfinal=None):
     bx, br, bi, bA = np.zeros((b, L, D)), np.zeros((b, L, D)), np.zeros((b, L, D)), np.zeros(D)
     for t in range(L - 1, -1, -1):
         before = h[:, t - 1] if t else (np.zeros((b, D)) if h0 is None else h0)
-        g = dh[:, t] + c
+        after = c
+        g = dh[:, t] + after
         gerr = err + U * STEP * np.abs(g)
         p, q = a[:, t] * before, a[:, t] ** 2 * inv[:, t] * si[:, t] * x[:, t]
         dL = g * (p - q)
@@ -84,7 +85,9 @@ def glr_backward(x, r, i, A, h, dh, h0=None, dfinal=None):
         br[:, t] = lerr * np.abs(Lg[:, t]) * (1 - sr[:, t]) + U * GATE * np.abs(dr[:, t])
         bA += (lerr * sr[:, t] + U * (GATE + L + 8 * b) * np.abs(dL * sr[:, t])).sum(0)
         c = a[:, t] * g
-        err = a[:, t] * gerr + U * (GATE * np.abs(u[:, t] * g) + STEP * np.abs(c))
+        # a link of the chain is a_t c_{t+1} + a_t dh_t, regrouped over tiles (A c + C): its products are rounded
+        # one by one, each within U of its own size, before the sum may cancel
+        err = a[:, t] * gerr + U * (GATE * np.abs(u[:, t] * g) + STEP * a[:, t] * (np.abs(after) + np.abs(dh[:, t])))
     return (dict(dx=dx, dr=dr, di=di, dA=dA, dh0=c),
             dict(dx=bx, dr=br, di=bi, dA=bA, dh0=err))
 

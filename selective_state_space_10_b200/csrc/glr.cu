@@ -35,12 +35,13 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
   return r;
 }
 
-// a = exp(L) and 1 - a^2 for L <= 0.  Near zero u = exp(L) - 1 comes from its Taylor series
-// (the first term left out is below 0.5^8 / 9! = 1e-8 of the sum), so that a = 1 + u and
-// 1 - a^2 = -u (2 + u) keep full relative precision for decays close to 1; an exp(L) rounded
-// near 1 and subtracted would not, and its error would be carried through every step of a
-// long memory.  Further away the exponential itself keeps a small a precise.
-__device__ __forceinline__ void decay(float L, float &a, float &rest) {
+// a = exp(L) for L <= 0, in one register: a itself where L < -0.5, else u = a - 1 (<= 0).  Near
+// zero u comes from its Taylor series (the first term left out is below 0.5^8 / 9! = 1e-8 of
+// the sum), so that a = 1 + u and 1 - a^2 = -u (2 + u) keep full relative precision for decays
+// close to 1; an exp(L) rounded near 1 and subtracted would not, and its error would be
+// carried through every step of a long memory.  Further away the exponential itself keeps a
+// small a precise (the floor of 1e-37 keeps it positive, hence recognisable).
+__device__ __forceinline__ float pack_decay(float L) {
   float p = 1.f / 40320.f;
   p = fmaf(p, L, 1.f / 5040.f);
   p = fmaf(p, L, 1.f / 720.f);
@@ -49,11 +50,12 @@ __device__ __forceinline__ void decay(float L, float &a, float &rest) {
   p = fmaf(p, L, 1.f / 6.f);
   p = fmaf(p, L, 0.5f);
   p = fmaf(p, L, 1.f);
-  p *= L;
-  const bool far = L < -0.5f;
-  const float e = ex2(L * kLog2e), u = far ? e - 1.f : p;
-  a = far ? e : 1.f + p;
-  rest = -u * (2.f + u);
+  return L < -0.5f ? fmaxf(ex2(L * kLog2e), 1e-37f) : p * L;
+}
+__device__ __forceinline__ float packed_a(float w) { return w > 0.f ? w : 1.f + w; }
+__device__ __forceinline__ float packed_rest(float w) {  // 1 - a^2
+  const float u = w > 0.f ? w - 1.f : w;
+  return -u * (2.f + u);
 }
 
 // The smaller of sigmoid(v) and sigmoid(-v); the other is one minus it.  exp(-|v|) cannot
@@ -68,11 +70,28 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// One step back: c (in: c_{t+1}, out: c_t = a_t g_t), the gradients of x, r and i, and dA's term.
+// dx = g beta si; di = dx x (1 - si); dL = g (a h_{t-1} - a^2 / beta si x); dr = dL L (1 - sr).
+// Where beta is 0 (a = 1) its slope's term is taken as 0.
+__device__ __forceinline__ void slopes(float A, float w, float zr, float r, float i, float x, float before, float dh,
+                                       float &c, float &dx, float &dr, float &di, float &dA) {
+  const float a = packed_a(w), rest = packed_rest(w);
+  const float inv = rest > 1e-37f ? rsqrt_approx(rest) : 0.f, beta = rest * inv;
+  const float zi = sigmoid_small(i), six = pick(i, zi), sr = pick(r, zr);
+  const float g = dh + c;
+  c = a * g;
+  dx = g * beta * six;
+  di = dx * x * pick(-i, zi);
+  const float dL = c * (before - a * inv * six * x);
+  dr = dL * (A * sr) * pick(-r, zr);
+  dA = fmaf(dL, sr, dA);
+}
+
 // One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x.
 __device__ __forceinline__ void gate(float x, float r, float i, float A, float &a, float &b) {
-  float rest;
-  decay(A * pick(r, sigmoid_small(r)), a, rest);
-  b = sqrt_approx(rest) * pick(i, sigmoid_small(i)) * x;
+  const float w = pack_decay(A * pick(r, sigmoid_small(r)));
+  a = packed_a(w);
+  b = sqrt_approx(packed_rest(w)) * pick(i, sigmoid_small(i)) * x;
 }
 
 // The scans.  A CTA takes 64 channels (two a lane) of one batch row and walks the sequence in
@@ -305,37 +324,96 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
   h[s] = from_f32<T>(n);
 }
 
-// The reverse walk: c_t = a_t g_t with g_t = dh_t + c_{t+1}.
-template <typename T>
-__global__ void __launch_bounds__(128)
+// The reverse scan: c_t = a_t g_t with g_t = dh_t + c_{t+1}, that is c_t = a_t c_{t+1} + a_t dh_t, over
+// tiles from the sequence's end.  Of the gates only the decay is needed before the barrier; it is kept
+// with sigmoid(r), and the rest is formed when g is known.  A tile is 5 inputs deep, which leaves two CTAs
+// an SM for bf16 and one for fp32.
+template <typename T, int CW, bool kCluster>
+__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
     k_glr_backward(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                    const float *__restrict__ A, const float *__restrict__ init, const T *__restrict__ h,
                    const T *__restrict__ dh, const float *dfinal, T *__restrict__ dx, T *__restrict__ dr,
                    T *__restrict__ di, float *dinit, float *__restrict__ part, GlrDims d, int blocks) {
-  const int64_t b = blockIdx.x / blocks, c = (int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x;
-  if (c >= d.D) return;
-  const float Ac = A[c];
-  float carry = dfinal != nullptr ? dfinal[b * d.D + c] : 0.f, dA = 0.f;
-  for (int64_t t = d.L - 1; t >= 0; --t) {
-    const int64_t at = (b * d.L + t) * d.row + c, to = (b * d.L + t) * d.grad + c, o = (b * d.L + t) * d.D + c;
-    const float xv = to_f32(x[at]), rv = to_f32(r[at]), iv = to_f32(i[at]);
-    const float before = t > 0 ? to_f32(h[o - d.D]) : init != nullptr ? init[b * d.D + c] : 0.f;
-    const float zr = sigmoid_small(rv), zi = sigmoid_small(iv), sr = pick(rv, zr), si = pick(iv, zi);
-    const float Lt = Ac * sr;
-    float a, b2;
-    decay(Lt, a, b2);
-    const float inv = b2 > 1e-37f ? rsqrt_approx(b2) : 0.f, beta = b2 * inv;
-    const float g = to_f32(dh[o]) + carry;
-    const float gx = g * beta * si;
-    const float dL = g * (a * before - a * a * inv * si * xv);
-    dx[to] = from_f32<T>(gx);
-    di[to] = from_f32<T>(gx * xv * pick(-iv, zi));
-    dr[to] = from_f32<T>(dL * Lt * pick(-rv, zr));
-    dA = fmaf(dL, sr, dA);
-    carry = a * g;
+  extern __shared__ __align__(16) char raw[];
+  ScanSmem<T, 5> &sm = *reinterpret_cast<ScanSmem<T, 5> *>(raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = kCluster ? cluster_rank() : 0, ranks = kCluster ? cluster_size() : 1;
+  const int64_t blk = blockIdx.x / ranks, b = blk / blocks, c0 = blk % blocks * kCh, c = c0 + 2 * lane;
+  const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));
+  const float A0 = n > 0 ? A[c] : 0.f, A1 = n > 1 ? A[c + 1] : 0.f;
+  const int64_t tiles = (d.L + kTile * ranks - 1) / (kTile * ranks);
+  // the first of a warp's tokens, t .. t + 7; those below 0 lie before the sequence
+  auto first = [&](int64_t tile) { return d.L - ((tile * ranks + rank) * kTile + warp * kT) - kT; };
+  auto load = [&](int64_t tile) {
+    if (tile < tiles) {
+      const int64_t t = first(tile), at = b * d.L * d.row, o = b * d.L * d.D;
+      auto &in = sm.in[warp][tile & 1];
+      fetch<T, CW>(&in[0][0][0], r + at, t, d.L, d.row, c0, d.D, lane);
+      fetch<T, CW>(&in[1][0][0], dh + o, t, d.L, d.D, c0, d.D, lane);
+      fetch<T, CW>(&in[2][0][0], i + at, t, d.L, d.row, c0, d.D, lane);
+      fetch<T, CW>(&in[3][0][0], x + at, t, d.L, d.row, c0, d.D, lane);
+      fetch<T, CW>(&in[4][0][0], h + o, t - 1, d.L, d.D, c0, d.D, lane);  // h_{t-1}
+    }
+    commit_async();
+  };
+  load(0);
+  load(1);
+  if (warp == 0)
+    sm.links.carry[0][lane] =
+        dfinal != nullptr ? make_float4(n > 0 ? dfinal[b * d.D + c] : 0.f, n > 1 ? dfinal[b * d.D + c + 1] : 0.f, 0.f, 0.f)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (kCluster) sync_ranks();  // no rank writes to another that has not started
+  float2 s = make_float2(0.f, 0.f), dA = make_float2(0.f, 0.f);
+  for (int64_t tile = 0; tile < tiles; ++tile) {
+    const int par = tile & 1;
+    const int64_t t = first(tile);
+    wait_async<1>();
+    __syncwarp();
+    auto &in = sm.in[warp][par];
+    float2 code[kT], zr[kT];
+    float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
+#pragma unroll
+    for (int j = kT - 1; j >= 0; --j) {
+      const float2 rj = pair(&in[0][j][2 * lane]), gj = pair(&in[1][j][2 * lane]);
+      zr[j] = make_float2(sigmoid_small(rj.x), sigmoid_small(rj.y));
+      code[j] = t + j >= 0 ? make_float2(pack_decay(A0 * pick(rj.x, zr[j].x)), pack_decay(A1 * pick(rj.y, zr[j].y)))
+                           : make_float2(0.f, 0.f);
+      const float a0 = packed_a(code[j].x), a1 = packed_a(code[j].y);
+      all = then(all, make_float4(a0, a0 * gj.x, a1, a1 * gj.y));
+    }
+    s = enter<kCluster>(sm.links, par, warp, lane, rank, ranks, all);
+#pragma unroll
+    for (int j = kT - 1; j >= 0; --j) {
+      const float2 rj = pair(&in[0][j][2 * lane]), gj = pair(&in[1][j][2 * lane]), ij = pair(&in[2][j][2 * lane]),
+                   xj = pair(&in[3][j][2 * lane]);
+      float2 hj = pair(&in[4][j][2 * lane]);
+      if (t + j == 0 && init != nullptr)
+        hj = make_float2(n > 0 ? init[b * d.D + c] : 0.f, n > 1 ? init[b * d.D + c + 1] : 0.f);
+      float2 ox, oi, orr;
+      slopes(A0, code[j].x, zr[j].x, rj.x, ij.x, xj.x, hj.x, gj.x, s.x, ox.x, orr.x, oi.x, dA.x);
+      slopes(A1, code[j].y, zr[j].y, rj.y, ij.y, xj.y, hj.y, gj.y, s.y, ox.y, orr.y, oi.y, dA.y);
+      if (t + j >= 0) {
+        const int64_t to = (b * d.L + t + j) * d.grad + c;
+        store2<CW == 16>(dx + to, ox.x, ox.y, n);
+        store2<CW == 16>(dr + to, orr.x, orr.y, n);
+        store2<CW == 16>(di + to, oi.x, oi.y, n);
+      }
+    }
+    __syncwarp();
+    load(tile + 2);
+    if (warp == kW - 1 && rank == ranks - 1 && tile + 1 < tiles) leave<kCluster>(sm.links, par, lane, ranks, s);
   }
-  part[b * d.D + c] = dA;
-  if (dinit != nullptr) dinit[b * d.D + c] = carry;
+  if (dinit != nullptr && warp == kW - 1 && rank == ranks - 1) store2<false>(dinit + b * d.D + c, s.x, s.y, n);
+  // dA over the CTA's warps, in order
+  wait_async<0>();
+  __syncthreads();
+  float2 *sums = reinterpret_cast<float2 *>(raw);
+  sums[warp * 32 + lane] = dA;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kW; ++w) dA = make_float2(dA.x + sums[w * 32 + lane].x, dA.y + sums[w * 32 + lane].y);
+    store2<false>(part + (b * ranks + rank) * d.D + c, dA.x, dA.y, n);
+  }
 }
 
 // dA over the batch, in order.
@@ -400,18 +478,26 @@ cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T
   return cudaGetLastError();
 }
 
-size_t glr_backward_floats(const GlrDims &d) { return (size_t)d.b * d.D; }
+size_t glr_backward_floats(const GlrDims &d) { return (size_t)d.b * kMaxRanks * d.D; }
 
 template <typename T>
 cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float *A, const float *init, const T *h,
                                 const T *dh, const float *dfinal, T *dx, T *dr, T *di, float *dA, float *dinit,
                                 float *part, const GlrDims &d, cudaStream_t st) {
-  const int64_t blocks = (d.D + 127) / 128;
-  k_glr_backward<T><<<(unsigned)(blocks * d.b), 128, 0, st>>>(x, r, i, A, init, h, dh, dfinal, dx, dr, di, dinit, part,
-                                                              d, (int)blocks);
-  cudaError_t e = cudaGetLastError();
+  const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
+  constexpr int E = 16 / sizeof(T);
+  const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && wide(dh) && wide(dx) && wide(dr) && wide(di) &&
+                   d.D % E == 0 && d.row % E == 0 && d.grad % E == 0;
+  const int ranks = pick_ranks(ctas, d.L, sizeof(T) == 2 ? 2 : 1);
+  auto run = [&](auto *one, auto *many) {
+    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, sizeof(ScanSmem<T, 5>), st, x, r, i, A, init, h, dh,
+                        dfinal, dx, dr, di, dinit, part, d, (int)blocks);
+  };
+  constexpr int CW = sizeof(T) == 4 ? 4 : 0;
+  cudaError_t e = w16 ? run(k_glr_backward<T, 16, false>, k_glr_backward<T, 16, true>)
+                      : run(k_glr_backward<T, CW, false>, k_glr_backward<T, CW, true>);
   if (e != cudaSuccess) return e;
-  k_glr_sum<<<(unsigned)blocks, 128, 0, st>>>(part, dA, d.D, d.b);
+  k_glr_sum<<<(unsigned)((d.D + 127) / 128), 128, 0, st>>>(part, dA, d.D, d.b * ranks);
   return cudaGetLastError();
 }
 
