@@ -12,7 +12,37 @@ namespace ssd {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+// Arithmetic on two channels at a time: one instruction for both (the scans are as close to the issue limit as
+// to the memory's).
+struct f2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ f2 mk(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ f2 both(float x) { return mk(x, x); }
+__device__ __forceinline__ float2 split(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -24,88 +54,144 @@ __device__ __forceinline__ float rcp(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ float sqrt_approx(float v) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ float rsqrt_approx(float v) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// maximum and minimum that keep a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2 ex2(f2 v) {
+  const float2 s = split(v);
+  return mk(ex2(s.x), ex2(s.y));
+}
+__device__ __forceinline__ f2 rcp(f2 v) {
+  const float2 s = split(v);
+  return mk(rcp(s.x), rcp(s.y));
+}
+__device__ __forceinline__ f2 rsqrt_approx(f2 v) {
+  const float2 s = split(v);
+  return mk(rsqrt_approx(s.x), rsqrt_approx(s.y));
+}
 
-// a = exp(L) for L <= 0, in one register: a itself where L < -0.5, else u = a - 1 (<= 0).  Near
-// zero u comes from its Taylor series (the first term left out is below 0.5^8 / 9! = 1e-8 of
-// the sum), so that a = 1 + u and 1 - a^2 = -u (2 + u) keep full relative precision for decays
-// close to 1; an exp(L) rounded near 1 and subtracted would not, and its error would be
-// carried through every step of a long memory.  Further away the exponential itself keeps a
-// small a precise (the floor of 1e-37 keeps it positive, hence recognisable).
-__device__ __forceinline__ float pack_decay(float L) {
-  float p = 1.f / 40320.f;
-  p = fmaf(p, L, 1.f / 5040.f);
-  p = fmaf(p, L, 1.f / 720.f);
-  p = fmaf(p, L, 1.f / 120.f);
-  p = fmaf(p, L, 1.f / 24.f);
-  p = fmaf(p, L, 1.f / 6.f);
-  p = fmaf(p, L, 0.5f);
-  p = fmaf(p, L, 1.f);
-  return L < -0.5f ? fmaxf(ex2(L * kLog2e), 1e-37f) : p * L;
-}
-__device__ __forceinline__ float packed_a(float w) { return w > 0.f ? w : 1.f + w; }
-__device__ __forceinline__ float packed_rest(float w) {  // 1 - a^2
-  const float u = w > 0.f ? w - 1.f : w;
-  return -u * (2.f + u);
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTiny = 1e-37f;  // keeps a root's argument positive where 1 - a^2 is 0
+
+// exp(-v), with overflow to infinity; exp_neg_finite stops at 2^126, so that e / (1 + e) stays 1
+__device__ __forceinline__ f2 exp_neg(f2 v) { return ex2(v * both(-kLog2e)); }
+__device__ __forceinline__ f2 exp_neg_finite(f2 v) {
+  const float2 s = split(v * both(-kLog2e));
+  return mk(ex2(min_nan(s.x, 126.f)), ex2(min_nan(s.y, 126.f)));
 }
 
-// The smaller of sigmoid(v) and sigmoid(-v); the other is one minus it.  exp(-|v|) cannot
-// overflow, and neither side loses relative precision.
-__device__ __forceinline__ float sigmoid_small(float v) {
-  const float e = ex2(-fabsf(v) * kLog2e);
-  return e * rcp(1.f + e);
+// a = exp(L) and v = 1 - a for L <= 0, both to full relative precision: L = n ln 2 + f with |f| <= ln 2 / 2,
+// p = exp(f) - 1 by a polynomial (fitted with relative weights and p'(0) = 1; 1.6e-8 off at most, below half a
+// step of fp32), a = 2^n (1 + p), v = (1 - 2^n) - 2^n p.  1 - a^2 = v (1 + a) then loses nothing for decays close
+// to 1; an exp(L) rounded near 1 and subtracted would, and its error would be carried through every step of a
+// long memory.  The exponential unit, which the gates already fill, is not used.
+__device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
+  const float2 s = split(L);
+  L = mk(max_nan(s.x, -87.f), max_nan(s.y, -87.f));  // n >= -126
+  const f2 t = fma2(L, both(kLog2e), both(12582912.f));  // 1.5 * 2^23: the integer lands in the low bits
+  const f2 n = t + both(-12582912.f);
+  const f2 f = fma2(n, both(-0.6931471805599453f), L);
+  f2 p = both(-0.0013946497347205877f);
+  p = fma2(p, f, both(-0.00836661085486412f));
+  p = fma2(p, f, both(-0.04166628047823906f));
+  p = fma2(p, f, both(-0.1666654348373413f));
+  p = fma2(p, f, both(-0.5f));
+  p = fma2(p, f, both(-1.f)) * f;  // 1 - exp(f)
+  const float2 i = split(t);
+  const f2 two_n = mk(__int_as_float((__float_as_int(i.x) << 23) + 0x3f800000),
+                      __int_as_float((__float_as_int(i.y) << 23) + 0x3f800000));
+  a = two_n * fma2(p, both(-1.f), both(1.f));
+  v = fma2(two_n, p, fma2(two_n, both(-1.f), both(1.f)));
 }
-__device__ __forceinline__ float pick(float v, float small) { return v >= 0.f ? 1.f - small : small; }
+
+// One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x, as x rest / sqrt(rest (1 + e)^2) with
+// rest = 1 - a^2 and e = exp(-i): one root in place of a root and a reciprocal.  A shut input gate (e and its
+// square overflow) gives 0.
+__device__ __forceinline__ void gate(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b) {
+  f2 v;
+  decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
+  const f2 rest = v * (a + both(1.f)), o = exp_neg(i) + both(1.f);
+  b = x * rest * rsqrt_approx(o * o * (rest + both(kTiny)));
+}
+
+// One step back: c (in: c_{t+1}, out: c_t = a_t g_t), the gradients of x, r and i, and dA's term.
+// dx = g beta si; di = dx x (1 - si); dL = g (a h_{t-1} - a^2 / beta si x); dr = dL L (1 - sr).
+// Where beta is 0 (a = 1) its slope's term is taken as 0.
+__device__ __forceinline__ void slopes(f2 A, f2 a, f2 v, f2 r, f2 i, f2 x, f2 before, f2 dh, f2 &c, f2 &dx, f2 &dr,
+                                       f2 &di, f2 &dA) {
+  const f2 rest = v * (a + both(1.f));
+  const float2 q = split(rest);
+  const f2 inv = mk(q.x > kTiny ? rsqrt_approx(q.x) : 0.f, q.y > kTiny ? rsqrt_approx(q.y) : 0.f);
+  const f2 er = exp_neg_finite(r), ei = exp_neg_finite(i);
+  const f2 sr = rcp(er + both(1.f)), si = rcp(ei + both(1.f)), six = si * x;
+  const f2 g = dh + c, gb = g * (rest * inv);
+  c = a * g;
+  dx = gb * si;
+  di = gb * six * (ei * si);
+  const f2 dL = c * fma2(a * inv * six, both(-1.f), before), ds = dL * sr;
+  dr = ds * A * (er * sr);
+  dA = dA + ds;
+}
 
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// One step back: c (in: c_{t+1}, out: c_t = a_t g_t), the gradients of x, r and i, and dA's term.
-// dx = g beta si; di = dx x (1 - si); dL = g (a h_{t-1} - a^2 / beta si x); dr = dL L (1 - sr).
-// Where beta is 0 (a = 1) its slope's term is taken as 0.
-__device__ __forceinline__ void slopes(float A, float w, float zr, float r, float i, float x, float before, float dh,
-                                       float &c, float &dx, float &dr, float &di, float &dA) {
-  const float a = packed_a(w), rest = packed_rest(w);
-  const float inv = rest > 1e-37f ? rsqrt_approx(rest) : 0.f, beta = rest * inv;
-  const float zi = sigmoid_small(i), six = pick(i, zi), sr = pick(r, zr);
-  const float g = dh + c;
-  c = a * g;
-  dx = g * beta * six;
-  di = dx * x * pick(-i, zi);
-  const float dL = c * (before - a * inv * six * x);
-  dr = dL * (A * sr) * pick(-r, zr);
-  dA = fmaf(dL, sr, dA);
+__device__ __forceinline__ f2 load2(const float *p) {
+  f2 r;
+  r.v = *reinterpret_cast<const unsigned long long *>(p);
+  return r;
 }
-
-// One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x.
-__device__ __forceinline__ void gate(float x, float r, float i, float A, float &a, float &b) {
-  const float w = pack_decay(A * pick(r, sigmoid_small(r)));
-  a = packed_a(w);
-  b = sqrt_approx(packed_rest(w)) * pick(i, sigmoid_small(i)) * x;
+__device__ __forceinline__ f2 load2(const __nv_bfloat16 *p) {
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+  return mk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// The first n (0 .. 2) of two neighbouring channels, one by one.
+template <typename T>
+__device__ __forceinline__ f2 load_n(const T *p, int n) {
+  return mk(n > 0 ? to_f32(p[0]) : 0.f, n > 1 ? to_f32(p[1]) : 0.f);
+}
+// Out; kPair: the address is aligned for both and n is 0 or 2.
+template <bool kPair, typename T>
+__device__ __forceinline__ void store2(T *p, f2 f, int n) {
+  const float2 s = split(f);
+  if constexpr (kPair) {
+    if (n == 0) return;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2 *>(p) = s;
+    else
+      *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(s.x, s.y);
+  } else {
+    if (n > 0) p[0] = from_f32<T>(s.x);
+    if (n > 1) p[1] = from_f32<T>(s.y);
+  }
 }
 
 // The scans.  A CTA takes 64 channels (two a lane) of one batch row and walks the sequence in
 // tiles of 64 tokens, 8 a warp.  Each warp copies its own tokens of the next tiles into
 // shared memory (two stages) while it forms the gates of this one, keeps its 8 decays and
 // input terms in registers, and publishes what they do to a state, h -> A h + H, as one
-// float4 a lane.  After a barrier a warp applies the warps before it to the carried state and
-// runs its 8 steps: every array is read and written once.  Where the channels alone leave
-// the GPU idle, a cluster of up to 8 CTAs shares a sequence, a tile each in turn: the CTAs'
-// own A h + H go to the ranks behind them through distributed shared memory.
-constexpr int kW = 8;          // warps
-constexpr int kT = 8;          // tokens a warp
+// 16-byte word a lane.  After a barrier a warp applies the warps before it to the carried
+// state and runs its 8 steps: every array is read and written once.  Where the channels alone
+// leave the GPU idle, a cluster of up to 8 CTAs shares a sequence, a tile each in turn: the
+// CTAs' own A h + H go to the ranks behind them through distributed shared memory.
+constexpr int kW = 8;  // warps
+constexpr int kT = 8;  // tokens a warp
 constexpr int kTile = kW * kT;
-constexpr int kCh = 64;        // channels a CTA
+constexpr int kCh = 64;  // channels a CTA
 constexpr int kMaxRanks = 8;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -126,52 +212,40 @@ __device__ __forceinline__ void wait_async() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's copy of rows t .. t + 7 (of those in [0, L)) of 64 channels from c0 on.  `base` is
-// the batch row's first element.  CW: bytes a copy (16 or 4), or 0 for element loads.
+// A lane's share of a warp's copies of 8 token rows of 64 channels from c0 on.  CW: bytes a
+// copy (16 or 4), or 0 for element loads.  The pointer follows the warp's rows from tile to
+// tile; rows outside [lo, hi) and channels outside the array arrive as zeros.
 template <typename T, int CW>
-__device__ __forceinline__ void fetch(T *dst, const T *base, int64_t t, int64_t L, int64_t stride, int64_t c0,
-                                      int64_t D, int lane) {
-  if constexpr (CW == 0) {
-#pragma unroll
-    for (int q = 0; q < kT * kCh / 32; ++q) {
-      const int row = q * 32 / kCh, c = q * 32 % kCh + lane;
-      const int64_t tt = t + row;
-      const bool valid = tt >= 0 && tt < L && c0 + c < D;
-      dst[row * kCh + c] = valid ? base[tt * stride + c0 + c] : T(0.f);
-    }
-  } else {
-    constexpr int E = CW / (int)sizeof(T), CPR = kCh / E, N = kT * CPR / 32;  // elements a copy, copies a row
-    const uint32_t to = smem_addr(dst) + lane * CW;
+struct Rows {
+  static constexpr int E = CW > 0 ? CW / (int)sizeof(T) : 1;  // elements a copy
+  static constexpr int CPR = kCh / E;                         // copies a row
+  static constexpr int N = kT * CPR / 32;                     // copies a lane
+  const T *p;
+  __device__ __forceinline__ static int row(int q, int lane) {
+    return CPR <= 32 ? q * (32 / CPR) + lane / CPR : q / (CPR / 32);
+  }
+  __device__ __forceinline__ static int chan(int q, int lane) {
+    return (CPR <= 32 ? lane % CPR : q % (CPR / 32) * 32 + lane) * E;
+  }
+  // t0: the warp's first token of the first tile (any integer: rows before the array are never read)
+  __device__ __forceinline__ void start(const T *base, int64_t t0, int64_t stride, int64_t c0, int lane) {
+    p = base + (t0 + row(0, lane)) * stride + c0 + chan(0, lane);
+  }
+  // channels: D - c0
+  __device__ __forceinline__ void fetch(T *dst, int lo, int hi, int64_t stride, int64_t channels, int lane) const {
+    const uint32_t to = smem_addr(dst) + lane * E * (int)sizeof(T);
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      const int row = CPR <= 32 ? q * (32 / CPR) + lane / CPR : q / (CPR / 32);
-      const int c = (CPR <= 32 ? lane % CPR : q % (CPR / 32) * 32 + lane) * E;
-      const int64_t tt = t + row;
-      const bool valid = tt >= 0 && tt < L && c0 + c < D;
-      copy_async<CW>(to + q * 32 * CW, valid ? base + tt * stride + c0 + c : base, valid);
+      const int j = row(q, lane);
+      const bool valid = j >= lo && j < hi && chan(q, lane) < channels;
+      const T *from = p + (row(q, 0) - row(0, 0)) * stride + (chan(q, 0) - chan(0, 0));
+      if constexpr (CW == 0)
+        dst[q * 32 + lane] = valid ? *from : T(0.f);
+      else
+        copy_async<CW>(to + q * 32 * CW, from, valid);
     }
   }
-}
-
-__device__ __forceinline__ float2 pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-__device__ __forceinline__ float2 pair(const __nv_bfloat16 *p) {
-  const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-// Two neighbouring channels out; kPair: the address is aligned for both and both exist.
-template <bool kPair, typename T>
-__device__ __forceinline__ void store2(T *p, float u, float v, int n) {
-  if constexpr (kPair) {
-    if (n < 2) return;
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float2 *>(p) = make_float2(u, v);
-    else
-      *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(u, v);
-  } else {
-    if (n > 0) p[0] = from_f32<T>(u);
-    if (n > 1) p[1] = from_f32<T>(v);
-  }
-}
+};
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -183,59 +257,64 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-// A barrier of the cluster: every write to distributed shared memory before it is seen after.
-__device__ __forceinline__ void sync_ranks() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// The cluster's barrier.  What a warp has written to distributed shared memory before a releasing arrival is seen
+// after the wait; warps that wrote nothing there arrive relaxed, and do not wait for their stores to drain.
+__device__ __forceinline__ void arrive_ranks(bool release) {
+  if (release)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void store_rank(void *p, uint32_t rank, float4 v) {
+__device__ __forceinline__ void wait_ranks() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// A state update h -> A h + H of a lane's two channels.
+struct alignas(16) Link {
+  f2 A, H;
+};
+__device__ __forceinline__ Link then(Link first, Link second) {
+  return {first.A * second.A, fma2(second.A, first.H, second.H)};
+}
+__device__ __forceinline__ void store_rank(Link *p, uint32_t rank, Link v) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
-
-// State updates h -> A h + H of two channels {A0, H0, A1, H1}: `second` after `first`.
-__device__ __forceinline__ float4 then(float4 first, float4 second) {
-  return make_float4(first.x * second.x, fmaf(second.x, first.y, second.y), first.z * second.z,
-                     fmaf(second.z, first.w, second.w));
-}
-__device__ __forceinline__ float2 apply(float4 f, float2 h) {
-  return make_float2(fmaf(f.x, h.x, f.y), fmaf(f.z, h.y, f.w));
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(a), "l"(v.A.v), "l"(v.H.v) : "memory");
 }
 
 // What the warps and ranks of a scan tell one another, by parity of the tile.
 struct Links {
-  float4 warp[2][kW][32];
-  float4 rank[2][kMaxRanks][32];
-  float4 carry[2][32];  // x, y: the state entering the tile
+  Link warp[2][kW][32];
+  Link rank[2][kMaxRanks][32];
+  Link carry[2][32];  // H: the state entering the tile
 };
 
-// The state entering this warp's tokens, given its own update `mine`; all ranks call it once a tile.
-template <bool kCluster>
-__device__ __forceinline__ float2 enter(Links &l, int par, int warp, int lane, int rank, int ranks, float4 mine) {
+// The state entering this warp's tokens, given its own update `mine`; all ranks call it once a tile.  `meanwhile`
+// runs while the ranks wait for one another.
+template <bool kCluster, typename F>
+__device__ __forceinline__ f2 enter(Links &l, int par, int warp, int lane, int rank, int ranks, Link mine, F meanwhile) {
   l.warp[par][warp][lane] = mine;
+  if constexpr (!kCluster) meanwhile();
   __syncthreads();
-  float4 before = make_float4(1.f, 0.f, 1.f, 0.f);
+  Link before = {both(1.f), both(0.f)};
   for (int w = 0; w < warp; ++w) before = then(before, l.warp[par][w][lane]);
   if constexpr (kCluster) {
     if (warp == kW - 1) {
-      const float4 all = then(before, mine);
+      const Link all = then(before, mine);
       for (int k = rank + 1; k < ranks; ++k) store_rank(&l.rank[par][rank][lane], k, all);
     }
-    sync_ranks();
+    arrive_ranks(warp == kW - 1);
+    meanwhile();
+    wait_ranks();
   }
-  const float4 c = l.carry[par][lane];
-  float2 h = make_float2(c.x, c.y);
+  f2 h = l.carry[par][lane].H;
   if constexpr (kCluster)
-    for (int k = 0; k < rank; ++k) h = apply(l.rank[par][k][lane], h);
-  return apply(before, h);
+    for (int k = 0; k < rank; ++k) h = fma2(l.rank[par][k][lane].A, h, l.rank[par][k][lane].H);
+  return fma2(before.A, h, before.H);
 }
 // The state after the tile's last token, from the last warp of the last rank, for the next tile (not
 // after the last one: a rank may have left by then).
 template <bool kCluster>
-__device__ __forceinline__ void leave(Links &l, int par, int lane, int ranks, float2 h) {
-  const float4 v = make_float4(h.x, h.y, 0.f, 0.f);
+__device__ __forceinline__ void leave(Links &l, int par, int lane, int ranks, f2 h) {
+  const Link v = {both(0.f), h};
   if constexpr (kCluster)
     for (int k = 0; k < ranks; ++k) store_rank(&l.carry[par ^ 1][lane], k, v);
   else
@@ -248,6 +327,26 @@ struct ScanSmem {
   Links links;
 };
 
+// A CTA's place in the grid.
+struct Place {
+  int warp, lane, rank, ranks, n;  // n: channels of this lane
+  int64_t b, c0, c;
+};
+template <bool kCluster>
+__device__ __forceinline__ Place place(int64_t D, int blocks) {
+  Place p;
+  p.warp = threadIdx.x / 32;
+  p.lane = threadIdx.x % 32;
+  p.rank = kCluster ? cluster_rank() : 0;
+  p.ranks = kCluster ? cluster_size() : 1;
+  const unsigned blk = blockIdx.x / p.ranks;
+  p.b = blk / blocks;
+  p.c0 = (int64_t)(blk % blocks) * kCh;
+  p.c = p.c0 + 2 * p.lane;
+  p.n = (int)max((int64_t)0, min((int64_t)2, D - p.c));
+  return p;
+}
+
 template <typename T, int CW, bool kCluster>
 __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 3 : 2)
     k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
@@ -255,58 +354,62 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 3 : 2)
                   int blocks) {
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 3> &sm = *reinterpret_cast<ScanSmem<T, 3> *>(raw);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rank = kCluster ? cluster_rank() : 0, ranks = kCluster ? cluster_size() : 1;
-  const int64_t blk = blockIdx.x / ranks, b = blk / blocks, c0 = blk % blocks * kCh, c = c0 + 2 * lane;
-  const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));  // channels of this lane
-  const float A0 = n > 0 ? A[c] : 0.f, A1 = n > 1 ? A[c + 1] : 0.f;
-  const T *const in[3] = {x + b * d.L * d.row, r + b * d.L * d.row, i + b * d.L * d.row};
-  const int64_t tiles = (d.L + kTile * ranks - 1) / (kTile * ranks);
-  auto first = [&](int64_t tile) { return (tile * ranks + rank) * kTile + warp * kT; };
-  auto load = [&](int64_t tile) {
-    if (tile < tiles) {
+  const Place p = place<kCluster>(d.D, blocks);
+  const f2 Ac = load_n(A + p.c, p.n);
+  const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
+  const int64_t t0 = p.rank * kTile + p.warp * kT;  // this warp's first token
+  int64_t left = d.L - t0;                          // tokens from it to the end
+  Rows<T, CW> rows[3];
+  rows[0].start(x + p.b * d.L * d.row, t0, d.row, p.c0, p.lane);
+  rows[1].start(r + p.b * d.L * d.row, t0, d.row, p.c0, p.lane);
+  rows[2].start(i + p.b * d.L * d.row, t0, d.row, p.c0, p.lane);
+  auto load = [&](int stage, int64_t rest) {  // rest: tokens of the sequence from the first row on
+    if (rest > 0) {
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
-        fetch<T, CW>(&sm.in[warp][tile & 1][k][0][0], in[k], first(tile), d.L, d.row, c0, d.D, lane);
+      for (int k = 0; k < 3; ++k) {
+        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], 0, (int)min(rest, (int64_t)kT), d.row, d.D - p.c0, p.lane);
+        rows[k].p += step * d.row;
+      }
     }
     commit_async();
   };
-  load(0);
-  load(1);
-  if (warp == 0)
-    sm.links.carry[0][lane] = init != nullptr ? make_float4(n > 0 ? init[b * d.D + c] : 0.f,
-                                                            n > 1 ? init[b * d.D + c + 1] : 0.f, 0.f, 0.f)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-  if constexpr (kCluster) sync_ranks();  // no rank writes to another that has not started
-  float2 s = make_float2(0.f, 0.f);
-  for (int64_t tile = 0; tile < tiles; ++tile) {
+  load(0, left);
+  load(1, left - step);
+  if (p.warp == 0) sm.links.carry[0][p.lane].H = init != nullptr ? load_n(init + p.b * d.D + p.c, p.n) : both(0.f);
+  if constexpr (kCluster) {  // no rank writes to another that has not started
+    arrive_ranks(true);
+    wait_ranks();
+  }
+  T *out = h + (p.b * d.L + t0) * d.D + p.c;
+  f2 s = both(0.f);
+  for (int64_t tile = 0; tile < tiles; ++tile, left -= step, out += step * d.D) {
     const int par = tile & 1;
-    const int64_t t = first(tile);
     wait_async<1>();
     __syncwarp();
-    float2 a[kT], v[kT];
-    float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
+    f2 a[kT], v[kT];
+    const auto &in = sm.in[p.warp][par];
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
-      const float2 xj = pair(&sm.in[warp][par][0][j][2 * lane]), rj = pair(&sm.in[warp][par][1][j][2 * lane]),
-                   ij = pair(&sm.in[warp][par][2][j][2 * lane]);
-      gate(xj.x, rj.x, ij.x, A0, a[j].x, v[j].x);
-      gate(xj.y, rj.y, ij.y, A1, a[j].y, v[j].y);
-      if (t + j >= d.L) a[j] = make_float2(1.f, 1.f), v[j] = make_float2(0.f, 0.f);
-      all = then(all, make_float4(a[j].x, v[j].x, a[j].y, v[j].y));
+    for (int j = 0; j < kT; ++j)
+      gate(load2(&in[0][j][2 * p.lane]), load2(&in[1][j][2 * p.lane]), load2(&in[2][j][2 * p.lane]), Ac, a[j], v[j]);
+    if (left < kT) {  // the sequence ends within these tokens: the rest leave the state as it is
+#pragma unroll
+      for (int j = 0; j < kT; ++j)
+        if (j >= left) a[j] = both(1.f), v[j] = both(0.f);
     }
+    Link all = {a[0], v[0]};
+#pragma unroll
+    for (int j = 1; j < kT; ++j) all = then(all, {a[j], v[j]});
     __syncwarp();
-    load(tile + 2);
-    s = enter<kCluster>(sm.links, par, warp, lane, rank, ranks, all);
-    T *out = h + (b * d.L + t) * d.D + c;
+    s = enter<kCluster>(sm.links, par, p.warp, p.lane, p.rank, p.ranks, all, [&] { load(par, left - 2 * step); });
 #pragma unroll
     for (int j = 0; j < kT; ++j) {
-      s = make_float2(fmaf(a[j].x, s.x, v[j].x), fmaf(a[j].y, s.y, v[j].y));
-      if (t + j < d.L) store2<CW == 16>(out + j * d.D, s.x, s.y, n);
+      s = fma2(a[j], s, v[j]);
+      if (j < left) store2<CW == 16>(out + j * d.D, s, p.n);
     }
-    if (warp == kW - 1 && rank == ranks - 1 && tile + 1 < tiles) leave<kCluster>(sm.links, par, lane, ranks, s);
+    if (p.warp == kW - 1 && p.rank == p.ranks - 1 && tile + 1 < tiles)
+      leave<kCluster>(sm.links, par, p.lane, p.ranks, s);
   }
-  if (warp == kW - 1 && rank == ranks - 1) store2<false>(final_state + b * d.D + c, s.x, s.y, n);
+  if (p.warp == kW - 1 && p.rank == p.ranks - 1) store2<false>(final_state + p.b * d.D + p.c, s, p.n);
 }
 
 template <typename T>
@@ -314,20 +417,20 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
                                                     const T *__restrict__ r, const T *__restrict__ i,
                                                     const float *__restrict__ A, T *__restrict__ h, GlrDims d,
                                                     int blocks) {
-  const int64_t b = blockIdx.x / blocks, c = (int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x;
-  if (c >= d.D) return;
+  const int64_t b = blockIdx.x / blocks, c = ((int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x) * 2;
+  const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));
   const int64_t at = b * d.row + c, s = b * d.D + c;
-  float a, v;
-  gate(to_f32(x[at]), to_f32(r[at]), to_f32(i[at]), A[c], a, v);
-  const float n = fmaf(a, state[s], v);
-  state[s] = n;
-  h[s] = from_f32<T>(n);
+  f2 a, v;
+  gate(load_n(x + at, n), load_n(r + at, n), load_n(i + at, n), load_n(A + c, n), a, v);
+  const f2 next = fma2(a, load_n(state + s, n), v);
+  store2<false>(state + s, next, n);
+  store2<false>(h + s, next, n);
 }
 
 // The reverse scan: c_t = a_t g_t with g_t = dh_t + c_{t+1}, that is c_t = a_t c_{t+1} + a_t dh_t, over
-// tiles from the sequence's end.  Of the gates only the decay is needed before the barrier; it is kept
-// with sigmoid(r), and the rest is formed when g is known.  A tile is 5 inputs deep, which leaves two CTAs
-// an SM for bf16 and one for fp32.
+// tiles from the sequence's end.  Of the gates only the decay is needed before the barrier; it is kept,
+// and the rest is formed when g is known.  A tile is 5 inputs deep, which leaves two CTAs an SM for bf16
+// and one for fp32.
 template <typename T, int CW, bool kCluster>
 __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
     k_glr_backward(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
@@ -336,87 +439,93 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
                    T *__restrict__ di, float *dinit, float *__restrict__ part, GlrDims d, int blocks) {
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 5> &sm = *reinterpret_cast<ScanSmem<T, 5> *>(raw);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rank = kCluster ? cluster_rank() : 0, ranks = kCluster ? cluster_size() : 1;
-  const int64_t blk = blockIdx.x / ranks, b = blk / blocks, c0 = blk % blocks * kCh, c = c0 + 2 * lane;
-  const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));
-  const float A0 = n > 0 ? A[c] : 0.f, A1 = n > 1 ? A[c + 1] : 0.f;
-  const int64_t tiles = (d.L + kTile * ranks - 1) / (kTile * ranks);
-  // the first of a warp's tokens, t .. t + 7; those below 0 lie before the sequence
-  auto first = [&](int64_t tile) { return d.L - ((tile * ranks + rank) * kTile + warp * kT) - kT; };
-  auto load = [&](int64_t tile) {
-    if (tile < tiles) {
-      const int64_t t = first(tile), at = b * d.L * d.row, o = b * d.L * d.D;
-      auto &in = sm.in[warp][tile & 1];
-      fetch<T, CW>(&in[0][0][0], r + at, t, d.L, d.row, c0, d.D, lane);
-      fetch<T, CW>(&in[1][0][0], dh + o, t, d.L, d.D, c0, d.D, lane);
-      fetch<T, CW>(&in[2][0][0], i + at, t, d.L, d.row, c0, d.D, lane);
-      fetch<T, CW>(&in[3][0][0], x + at, t, d.L, d.row, c0, d.D, lane);
-      fetch<T, CW>(&in[4][0][0], h + o, t - 1, d.L, d.D, c0, d.D, lane);  // h_{t-1}
+  const Place p = place<kCluster>(d.D, blocks);
+  const f2 Ac = load_n(A + p.c, p.n);
+  const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
+  // this warp's tokens are t .. t + 7; those below 0 lie before the sequence
+  int64_t t = d.L - kT - (p.rank * kTile + p.warp * kT);
+  Rows<T, CW> rows[5];  // r, dh, i, x, h_{t-1}
+  const int64_t at = p.b * d.L * d.row, o = p.b * d.L * d.D;
+  rows[0].start(r + at, t, d.row, p.c0, p.lane);
+  rows[1].start(dh + o, t, d.D, p.c0, p.lane);
+  rows[2].start(i + at, t, d.row, p.c0, p.lane);
+  rows[3].start(x + at, t, d.row, p.c0, p.lane);
+  rows[4].start(h + o, t - 1, d.D, p.c0, p.lane);
+  auto load = [&](int stage, int64_t t) {
+    if (t > -kT) {
+#pragma unroll
+      for (int k = 0; k < 5; ++k) {
+        const int64_t stride = k == 1 || k == 4 ? d.D : d.row;
+        const int lo = (int)max((int64_t)0, (k == 4 ? 1 : 0) - t);
+        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], lo, kT, stride, d.D - p.c0, p.lane);
+        rows[k].p -= step * stride;
+      }
     }
     commit_async();
   };
-  load(0);
-  load(1);
-  if (warp == 0)
-    sm.links.carry[0][lane] =
-        dfinal != nullptr ? make_float4(n > 0 ? dfinal[b * d.D + c] : 0.f, n > 1 ? dfinal[b * d.D + c + 1] : 0.f, 0.f, 0.f)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-  if constexpr (kCluster) sync_ranks();  // no rank writes to another that has not started
-  float2 s = make_float2(0.f, 0.f), dA = make_float2(0.f, 0.f);
-  for (int64_t tile = 0; tile < tiles; ++tile) {
+  load(0, t);
+  load(1, t - step);
+  if (p.warp == 0) sm.links.carry[0][p.lane].H = dfinal != nullptr ? load_n(dfinal + p.b * d.D + p.c, p.n) : both(0.f);
+  if constexpr (kCluster) {  // no rank writes to another that has not started
+    arrive_ranks(true);
+    wait_ranks();
+  }
+  int64_t to = (p.b * d.L + t) * d.grad + p.c;
+  f2 s = both(0.f), dA = both(0.f);
+  for (int64_t tile = 0; tile < tiles; ++tile, t -= step, to -= step * d.grad) {
     const int par = tile & 1;
-    const int64_t t = first(tile);
     wait_async<1>();
     __syncwarp();
-    auto &in = sm.in[warp][par];
-    float2 code[kT], zr[kT];
-    float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
+    const auto &in = sm.in[p.warp][par];
+    f2 a[kT], v[kT];
 #pragma unroll
-    for (int j = kT - 1; j >= 0; --j) {
-      const float2 rj = pair(&in[0][j][2 * lane]), gj = pair(&in[1][j][2 * lane]);
-      zr[j] = make_float2(sigmoid_small(rj.x), sigmoid_small(rj.y));
-      code[j] = t + j >= 0 ? make_float2(pack_decay(A0 * pick(rj.x, zr[j].x)), pack_decay(A1 * pick(rj.y, zr[j].y)))
-                           : make_float2(0.f, 0.f);
-      const float a0 = packed_a(code[j].x), a1 = packed_a(code[j].y);
-      all = then(all, make_float4(a0, a0 * gj.x, a1, a1 * gj.y));
+    for (int j = kT - 1; j >= 0; --j)
+      decay(Ac * rcp(exp_neg(load2(&in[0][j][2 * p.lane])) + both(1.f)), a[j], v[j]);
+    if (t < 0) {  // tokens before the first leave c as it is
+#pragma unroll
+      for (int j = 0; j < kT; ++j)
+        if (t + j < 0) a[j] = both(1.f), v[j] = both(0.f);
     }
-    s = enter<kCluster>(sm.links, par, warp, lane, rank, ranks, all);
+    Link all = {both(1.f), both(0.f)};
+    const bool any = t > -kT;  // a warp wholly before the sequence has fetched nothing
+    if (any) {
+#pragma unroll
+      for (int j = kT - 1; j >= 0; --j) all = then(all, {a[j], a[j] * load2(&in[1][j][2 * p.lane])});
+    }
+    s = enter<kCluster>(sm.links, par, p.warp, p.lane, p.rank, p.ranks, all, [] {});
 #pragma unroll
     for (int j = kT - 1; j >= 0; --j) {
-      const float2 rj = pair(&in[0][j][2 * lane]), gj = pair(&in[1][j][2 * lane]), ij = pair(&in[2][j][2 * lane]),
-                   xj = pair(&in[3][j][2 * lane]);
-      float2 hj = pair(&in[4][j][2 * lane]);
-      if (t + j == 0 && init != nullptr)
-        hj = make_float2(n > 0 ? init[b * d.D + c] : 0.f, n > 1 ? init[b * d.D + c + 1] : 0.f);
-      float2 ox, oi, orr;
-      slopes(A0, code[j].x, zr[j].x, rj.x, ij.x, xj.x, hj.x, gj.x, s.x, ox.x, orr.x, oi.x, dA.x);
-      slopes(A1, code[j].y, zr[j].y, rj.y, ij.y, xj.y, hj.y, gj.y, s.y, ox.y, orr.y, oi.y, dA.y);
+      if (!any) break;
+      f2 before = load2(&in[4][j][2 * p.lane]);
+      if (t + j == 0 && init != nullptr) before = load_n(init + p.b * d.D + p.c, p.n);
+      f2 ox, orr, oi;
+      slopes(Ac, a[j], v[j], load2(&in[0][j][2 * p.lane]), load2(&in[2][j][2 * p.lane]), load2(&in[3][j][2 * p.lane]),
+             before, load2(&in[1][j][2 * p.lane]), s, ox, orr, oi, dA);
       if (t + j >= 0) {
-        const int64_t to = (b * d.L + t + j) * d.grad + c;
-        store2<CW == 16>(dx + to, ox.x, ox.y, n);
-        store2<CW == 16>(dr + to, orr.x, orr.y, n);
-        store2<CW == 16>(di + to, oi.x, oi.y, n);
+        store2<CW == 16>(dx + to + j * d.grad, ox, p.n);
+        store2<CW == 16>(dr + to + j * d.grad, orr, p.n);
+        store2<CW == 16>(di + to + j * d.grad, oi, p.n);
       }
     }
     __syncwarp();
-    load(tile + 2);
-    if (warp == kW - 1 && rank == ranks - 1 && tile + 1 < tiles) leave<kCluster>(sm.links, par, lane, ranks, s);
+    load(par, t - 2 * step);
+    if (p.warp == kW - 1 && p.rank == p.ranks - 1 && tile + 1 < tiles)
+      leave<kCluster>(sm.links, par, p.lane, p.ranks, s);
   }
-  if (dinit != nullptr && warp == kW - 1 && rank == ranks - 1) store2<false>(dinit + b * d.D + c, s.x, s.y, n);
+  if (dinit != nullptr && p.warp == kW - 1 && p.rank == p.ranks - 1) store2<false>(dinit + p.b * d.D + p.c, s, p.n);
   // dA over the CTA's warps, in order
   wait_async<0>();
   __syncthreads();
-  float2 *sums = reinterpret_cast<float2 *>(raw);
-  sums[warp * 32 + lane] = dA;
+  f2 *sums = reinterpret_cast<f2 *>(raw);
+  sums[p.warp * 32 + p.lane] = dA;
   __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < kW; ++w) dA = make_float2(dA.x + sums[w * 32 + lane].x, dA.y + sums[w * 32 + lane].y);
-    store2<false>(part + (b * ranks + rank) * d.D + c, dA.x, dA.y, n);
+  if (p.warp == 0) {
+    for (int w = 1; w < kW; ++w) dA = dA + sums[w * 32 + p.lane];
+    store2<false>(part + (p.b * p.ranks + p.rank) * d.D + p.c, dA, p.n);
   }
 }
 
-// dA over the batch, in order.
+// dA over the batch and the ranks, in order.
 __global__ void __launch_bounds__(128) k_glr_sum(const float *__restrict__ part, float *__restrict__ dA, int64_t D,
                                                  int64_t n) {
   const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
@@ -425,8 +534,6 @@ __global__ void __launch_bounds__(128) k_glr_sum(const float *__restrict__ part,
   for (int64_t k = 0; k < n; ++k) s += part[k * D + c];
   dA[c] = s;
 }
-
-}  // namespace
 
 bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -454,6 +561,8 @@ cudaError_t launch_ranks(void (*f)(P...), int64_t ctas, int ranks, size_t smem, 
   return cudaLaunchKernelEx(&cfg, f, v...);
 }
 
+}  // namespace
+
 template <typename T>
 cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h,
                                float *final_state, const GlrDims &d, cudaStream_t st) {
@@ -473,7 +582,7 @@ cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *
 template <typename T>
 cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T *i, const float *A, T *h,
                                    const GlrDims &d, cudaStream_t st) {
-  const int64_t blocks = (d.D + 127) / 128;
+  const int64_t blocks = (d.D + 255) / 256;
   k_glr_decode<T><<<(unsigned)(blocks * d.b), 128, 0, st>>>(state, x, r, i, A, h, d, (int)blocks);
   return cudaGetLastError();
 }
