@@ -461,22 +461,43 @@ def wait_selftest(workspace, limit_ns: int = 1_000_000, expire: bool = True, str
     return prefill_device_status(workspace, stream)
 
 
-def _cuda(t: torch.Tensor, name: str) -> torch.device:
+# The calls below are short next to a decode step's host work: the checks first compare what
+# holds for every good call, and _check only words the refusal.
+
+def _cuda(t: torch.Tensor, name: str) -> int:
+    """The tensor's CUDA device index."""
     if t.dtype not in _DTYPES:
         raise ValueError(f"unsupported {name} dtype {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("libssd runs on CUDA tensors only")
-    return t.device
+    return t.get_device()
 
 
-def _call(where: str, dev: torch.device, stream, args) -> None:
+def _ok(t: torch.Tensor, name: str, shape, dtype, dev: int) -> None:
+    """A contiguous tensor of this shape and dtype on CUDA device `dev`."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        _check(t, name, shape, dtype, torch.device("cuda", dev))
+
+
+def _ok_f32(tensors, shape, dev: int) -> None:
+    for name, t in tensors:
+        if t is not None and (t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous() or
+                              t.get_device() != dev):
+            _check(t, name, shape, torch.float32, torch.device("cuda", dev))
+
+
+def _call(where: str, dev: int, stream, args) -> None:
     """fn(*args, stream) on the tensors' device, on `stream` or that device's current one."""
     fn = getattr(lib, where)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev) without its object
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
+            st = fn(*args, stream)
     if st != OK:
         raise SSDError(st, where)
 
@@ -485,11 +506,11 @@ def _address(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _row_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+def _row_stride(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
     """Elements between consecutive rows of a [..., D] array whose rows may be slices of wider
     ones: unit stride within a row, one stride from row to row over all leading axes."""
-    if t.device != device or t.dtype != dtype or t.shape != shape:
-        _check(t, name, shape, dtype, device)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _check(t, name, shape, dtype, torch.device("cuda", dev) if dev >= 0 else t.device)
     D = shape[-1]
     if t.is_contiguous():
         return D
@@ -508,21 +529,31 @@ def _row_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     return row
 
 
-def _same_stride(tensors, shape, dtype, device) -> int:
-    rows = [_row_stride(t, name, shape, dtype, device) for name, t in tensors]
-    many = 1
-    for k in shape[:-1]:
-        many *= k
-    if many > 1 and any(r != rows[0] for r in rows):
-        raise ValueError(f"{', '.join(n for n, _ in tensors)} must have the same row stride, got {rows}")
-    return rows[0]
+def _same_stride(names, x, r, i, shape, dtype, dev: int) -> int:
+    """The row stride that three arrays share (any of them where there is one row at most)."""
+    row = _row_stride(x, names[0], shape, dtype, dev)
+    for name, t in ((names[1], r), (names[2], i)):
+        other = _row_stride(t, name, shape, dtype, dev)
+        if other != row and shape[:-1].numel() > 1:
+            raise ValueError(f"{', '.join(names)} must have the same row stride, got {row} and {other}")
+    return row
 
 
-def _workspace(workspace, need: int, dev):
+_XRI, _GRADS = ("x", "r", "i"), ("dx", "dr", "di")
+
+
+def _new(like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """A contiguous tensor on like's device; empty_like is the quickest way to one."""
+    if like.shape == shape and like.dtype is dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(workspace, need: int, like: torch.Tensor):
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+        return like.new_empty(need, dtype=torch.uint8), need
+    if workspace.device != like.device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {like.device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -536,18 +567,15 @@ def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream
     dev = _cuda(x, "x")
     shape = x.shape
     b, L, D = shape
-    row = _same_stride((("x", x), ("r", r), ("i", i)), shape, x.dtype, dev)
-    _check(A, "A", (D,), torch.float32, dev)
-    if initial_state is not None:
-        _check(initial_state, "initial_state", (b, D), torch.float32, dev)
+    row = _same_stride(_XRI, x, r, i, shape, x.dtype, dev)
+    _ok(A, "A", (D,), torch.float32, dev)
     if h is None:
-        h = torch.empty(shape, dtype=x.dtype, device=dev)
+        h = _new(x, shape, x.dtype)
     else:
-        _check(h, "h", shape, x.dtype, dev)
+        _ok(h, "h", shape, x.dtype, dev)
     if final_state is None:
-        final_state = torch.empty((b, D), dtype=torch.float32, device=dev)
-    else:
-        _check(final_state, "final_state", (b, D), torch.float32, dev)
+        final_state = _new(A if initial_state is None else initial_state, (b, D), torch.float32)
+    _ok_f32((("initial_state", initial_state), ("final_state", final_state)), (b, D), dev)
     dims = GlrDims(b, L, D, row, D)
     _call("ssd_glr_prefill", dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
@@ -563,13 +591,13 @@ def glr_decode_step(state, x, r, i, A, h=None, stream=None) -> torch.Tensor:
     dev = _cuda(x, "x")
     shape = x.shape
     b, D = shape
-    row = _same_stride((("x", x), ("r", r), ("i", i)), shape, x.dtype, dev)
-    _check(A, "A", (D,), torch.float32, dev)
-    _check(state, "state", (b, D), torch.float32, dev)
+    row = _same_stride(_XRI, x, r, i, shape, x.dtype, dev)
+    _ok(A, "A", (D,), torch.float32, dev)
+    _ok(state, "state", shape, torch.float32, dev)
     if h is None:
-        h = torch.empty(shape, dtype=x.dtype, device=dev)
+        h = _new(x, shape, x.dtype)
     else:
-        _check(h, "h", shape, x.dtype, dev)
+        _ok(h, "h", shape, x.dtype, dev)
     dims = GlrDims(b, 1, D, row, D)
     _call("ssd_glr_decode_step", dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(),
@@ -587,27 +615,22 @@ def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=No
     dev = _cuda(x, "x")
     shape = x.shape
     b, L, D = shape
-    row = _same_stride((("x", x), ("r", r), ("i", i)), shape, x.dtype, dev)
-    _check(A, "A", (D,), torch.float32, dev)
-    _check(h, "h", shape, x.dtype, dev)
-    _check(dh, "dh", shape, x.dtype, dev)
-    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state),
-                    ("dinitial_state", dinitial_state)):
-        if t is not None:
-            _check(t, name, (b, D), torch.float32, dev)
-    dx = torch.empty(shape, dtype=x.dtype, device=dev) if dx is None else dx
-    dr = torch.empty(shape, dtype=x.dtype, device=dev) if dr is None else dr
-    di = torch.empty(shape, dtype=x.dtype, device=dev) if di is None else di
-    grad = _same_stride((("dx", dx), ("dr", dr), ("di", di)), shape, x.dtype, dev)
-    if dA is None:
-        dA = torch.empty(D, dtype=torch.float32, device=dev)
-    else:
-        _check(dA, "dA", (D,), torch.float32, dev)
+    row = _same_stride(_XRI, x, r, i, shape, x.dtype, dev)
+    _ok(h, "h", shape, x.dtype, dev)
+    _ok(dh, "dh", shape, x.dtype, dev)
+    dx = torch.empty_like(h) if dx is None else dx
+    dr = torch.empty_like(h) if dr is None else dr
+    di = torch.empty_like(h) if di is None else di
+    grad = _same_stride(_GRADS, dx, dr, di, shape, x.dtype, dev)
+    dA = torch.empty_like(A) if dA is None else dA
+    _ok_f32((("A", A), ("dA", dA)), (D,), dev)
     if dinitial_state is None:
-        dinitial_state = torch.empty((b, D), dtype=torch.float32, device=dev)
+        dinitial_state = _new(A if dfinal_state is None else dfinal_state, (b, D), torch.float32)
+    _ok_f32((("initial_state", initial_state), ("dfinal_state", dfinal_state), ("dinitial_state", dinitial_state)),
+            (b, D), dev)
     dims = GlrDims(b, L, D, row, grad)
     need = lib.ssd_glr_backward_workspace_size(ctypes.byref(dims), _DTYPES[x.dtype])
-    workspace, nbytes = _workspace(workspace, need, dev)
+    workspace, nbytes = _workspace(workspace, need, A)
     _call("ssd_glr_backward", dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
            _address(initial_state), h.data_ptr(), dh.data_ptr(), _address(dfinal_state), dx.data_ptr(),
@@ -633,25 +656,23 @@ def residual_norm(x, weight, residual=None, scale=None, residual_dtype=None, eps
     dev = _cuda(x, "x")
     shape = x.shape
     rows, D = _norm_rows(x, "x")
-    _check(x, "x", shape, x.dtype, dev)
+    _ok(x, "x", shape, x.dtype, dev)
     if residual_dtype is None:
         residual_dtype = residual.dtype if residual is not None else \
             residual_out.dtype if residual_out is not None else x.dtype
     if residual_dtype not in _DTYPES:
         raise ValueError(f"unsupported residual dtype {residual_dtype}")
-    _check(weight, "weight", (D,), torch.float32, dev)
-    if scale is not None:
-        _check(scale, "scale", (D,), torch.float32, dev)
+    _ok_f32((("weight", weight), ("scale", scale)), (D,), dev)
     if residual is not None:
-        _check(residual, "residual", shape, residual_dtype, dev)
+        _ok(residual, "residual", shape, residual_dtype, dev)
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual_dtype, device=dev)
+        residual_out = _new(x if residual is None else residual, shape, residual_dtype)
     else:
-        _check(residual_out, "residual_out", shape, residual_dtype, dev)
+        _ok(residual_out, "residual_out", shape, residual_dtype, dev)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)
     else:
-        _check(out, "out", shape, x.dtype, dev)
+        _ok(out, "out", shape, x.dtype, dev)
     dims = NormDims(rows, D, 1, D, D)
     _call("ssd_residual_norm", dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], _DTYPES[residual_dtype], x.data_ptr(), _address(scale),
@@ -669,28 +690,29 @@ def residual_norm_backward(dout, s, weight, x=None, scale=None, dresidual_out=No
         raise ValueError(f"unsupported s dtype {s.dtype}")
     shape = dout.shape
     rows, D = _norm_rows(dout, "dout")
-    _check(dout, "dout", shape, dout.dtype, dev)
-    _check(s, "s", shape, s.dtype, dev)
-    _check(weight, "weight", (D,), torch.float32, dev)
+    _ok(dout, "dout", shape, dout.dtype, dev)
+    _ok(s, "s", shape, s.dtype, dev)
     if dresidual_out is not None:
-        _check(dresidual_out, "dresidual_out", shape, s.dtype, dev)
+        _ok(dresidual_out, "dresidual_out", shape, s.dtype, dev)
     if scale is not None:
-        _check(scale, "scale", (D,), torch.float32, dev)
         if x is None:
             raise ValueError("the gradient of scale needs x")
-        _check(x, "x", shape, dout.dtype, dev)
-        dscale = torch.empty(D, dtype=torch.float32, device=dev) if dscale is None else dscale
-        _check(dscale, "dscale", (D,), torch.float32, dev)
+        _ok(x, "x", shape, dout.dtype, dev)
+        dscale = torch.empty_like(scale) if dscale is None else dscale
     elif dscale is not None:
         raise ValueError("dscale without a scale")
-    dx = torch.empty(shape, dtype=dout.dtype, device=dev) if dx is None else dx
-    dresidual = torch.empty(shape, dtype=s.dtype, device=dev) if dresidual is None else dresidual
-    dweight = torch.empty(D, dtype=torch.float32, device=dev) if dweight is None else dweight
-    _check(dx, "dx", shape, dout.dtype, dev)
-    _check(dresidual, "dresidual", shape, s.dtype, dev)
-    _check(dweight, "dweight", (D,), torch.float32, dev)
+    if dx is None:
+        dx = torch.empty_like(dout)
+    else:
+        _ok(dx, "dx", shape, dout.dtype, dev)
+    if dresidual is None:
+        dresidual = torch.empty_like(s)
+    else:
+        _ok(dresidual, "dresidual", shape, s.dtype, dev)
+    dweight = torch.empty_like(weight) if dweight is None else dweight
+    _ok_f32((("weight", weight), ("scale", scale), ("dweight", dweight), ("dscale", dscale)), (D,), dev)
     dims = NormDims(rows, D, 1, D, D)
-    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), dev)
+    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
     _call("ssd_residual_norm_backward", dev, stream,
           (ctypes.byref(dims), _DTYPES[dout.dtype], _DTYPES[s.dtype], _address(x if scale is not None else None),
            _address(scale), s.data_ptr(), weight.data_ptr(), eps, dout.data_ptr(), _address(dresidual_out),
@@ -709,13 +731,13 @@ def gated_norm(y, z, weight, ngroups: int = 1, gate_first: bool = True, eps: flo
         raise ValueError(f"unsupported y dtype {y.dtype}")
     shape = y.shape
     rows, D = _norm_rows(y, "y")
-    _check(y, "y", shape, y.dtype, dev)
+    _ok(y, "y", shape, y.dtype, dev)
     gate = _row_stride(z, "z", shape, z.dtype, dev)
-    _check(weight, "weight", (D,), torch.float32, dev)
+    _ok(weight, "weight", (D,), torch.float32, dev)
     if out is None:
-        out = torch.empty(shape, dtype=z.dtype, device=dev)
+        out = _new(z, shape, z.dtype)
     else:
-        _check(out, "out", shape, z.dtype, dev)
+        _ok(out, "out", shape, z.dtype, dev)
     dims = NormDims(rows, D, int(ngroups), gate, D)
     _call("ssd_gated_norm", dev, stream,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
@@ -732,18 +754,19 @@ def gated_norm_backward(dout, y, z, weight, ngroups: int = 1, gate_first: bool =
         raise ValueError(f"unsupported y dtype {y.dtype}")
     shape = y.shape
     rows, D = _norm_rows(y, "y")
-    _check(y, "y", shape, y.dtype, dev)
+    _ok(y, "y", shape, y.dtype, dev)
     gate = _row_stride(z, "z", shape, z.dtype, dev)
-    _check(dout, "dout", shape, z.dtype, dev)
-    _check(weight, "weight", (D,), torch.float32, dev)
-    dy = torch.empty(shape, dtype=y.dtype, device=dev) if dy is None else dy
-    dz = torch.empty(shape, dtype=z.dtype, device=dev) if dz is None else dz
-    dweight = torch.empty(D, dtype=torch.float32, device=dev) if dweight is None else dweight
-    _check(dy, "dy", shape, y.dtype, dev)
+    _ok(dout, "dout", shape, z.dtype, dev)
+    if dy is None:
+        dy = torch.empty_like(y)
+    else:
+        _ok(dy, "dy", shape, y.dtype, dev)
+    dz = torch.empty_like(dout) if dz is None else dz
     dgate = _row_stride(dz, "dz", shape, z.dtype, dev)
-    _check(dweight, "dweight", (D,), torch.float32, dev)
+    dweight = torch.empty_like(weight) if dweight is None else dweight
+    _ok_f32((("weight", weight), ("dweight", dweight)), (D,), dev)
     dims = NormDims(rows, D, int(ngroups), gate, dgate)
-    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), dev)
+    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
     _call("ssd_gated_norm_backward", dev, stream,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
            weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(),

@@ -155,7 +155,7 @@ def test_binding_refuses_bad_tensors(ssd):
         ssd.residual_norm(t.half(), torch.zeros(8))
     with pytest.raises(ValueError, match="must be \\[b,L,D\\]"):
         ssd.glr_prefill(t[0], t[0], t[0], torch.zeros(8))
-    dev, f = torch.device("cpu"), torch.float32
+    dev, f = -1, torch.float32  # a CPU tensor's get_device()
     row = lambda v: ssd._row_stride(v, "z", v.shape, f, dev)
     assert row(torch.zeros(2, 3, 24)[..., 8:16]) == 24
     assert row(torch.zeros(2, 1, 24)[..., 8:16]) == 24
@@ -167,6 +167,6 @@ def test_binding_refuses_bad_tensors(ssd):
             row(bad)
     a, b = torch.zeros(3, 24)[:, :8], torch.zeros(3, 16)[:, :8]
     with pytest.raises(ValueError, match="same row stride"):
-        ssd._same_stride((("x", a), ("r", b)), a.shape, f, dev)
+        ssd._same_stride(("x", "r", "i"), a, b, a, a.shape, f, dev)
     with pytest.raises(ValueError, match="shape"):
         ssd._row_stride(a, "z", (3, 9), f, dev)
