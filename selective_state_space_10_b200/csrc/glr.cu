@@ -4,61 +4,16 @@
 //
 // over whole sequences, for one token, and its gradients.
 #include <algorithm>
+#include <stdlib.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 
 namespace ssd {
 
 namespace {
 
-// Arithmetic on two channels at a time: one instruction for both (the scans are as close to the issue limit as
-// to the memory's).
-struct f2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ f2 mk(float x, float y) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ f2 both(float x) { return mk(x, x); }
-__device__ __forceinline__ float2 split(f2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rsqrt_approx(float v) {
-  float r;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 // maximum and minimum that keep a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -70,20 +25,6 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ f2 ex2(f2 v) {
-  const float2 s = split(v);
-  return mk(ex2(s.x), ex2(s.y));
-}
-__device__ __forceinline__ f2 rcp(f2 v) {
-  const float2 s = split(v);
-  return mk(rcp(s.x), rcp(s.y));
-}
-__device__ __forceinline__ f2 rsqrt_approx(f2 v) {
-  const float2 s = split(v);
-  return mk(rsqrt_approx(s.x), rsqrt_approx(s.y));
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTiny = 1e-37f;  // keeps a root's argument positive where 1 - a^2 is 0
 
 // exp(-v), with overflow to infinity; exp_neg_finite stops at 2^126, so that e / (1 + e) stays 1
@@ -146,18 +87,13 @@ __device__ __forceinline__ void slopes(f2 A, f2 a, f2 v, f2 r, f2 i, f2 x, f2 be
   dA = dA + ds;
 }
 
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
 __device__ __forceinline__ f2 load2(const float *p) {
   f2 r;
   r.v = *reinterpret_cast<const unsigned long long *>(p);
   return r;
 }
 __device__ __forceinline__ f2 load2(const __nv_bfloat16 *p) {
-  const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
-  return mk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  return from_bf16x2(*reinterpret_cast<const uint32_t *>(p));
 }
 // The first n (0 .. 2) of two neighbouring channels, one by one.
 template <typename T>
@@ -173,7 +109,7 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<float2 *>(p) = s;
     else
-      *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(s.x, s.y);
+      *reinterpret_cast<uint32_t *>(p) = to_bf16x2(f);
   } else {
     if (n > 0) p[0] = from_f32<T>(s.x);
     if (n > 1) p[1] = from_f32<T>(s.y);
@@ -188,9 +124,14 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
 // state and runs its 8 steps: every array is read and written once.  Where the channels alone
 // leave the GPU idle, a cluster of up to 8 CTAs shares a sequence, a tile each in turn: the
 // CTAs' own A h + H go to the ranks behind them through distributed shared memory.
-constexpr int kW = 8;  // warps
-constexpr int kT = 8;  // tokens a warp
-constexpr int kTile = kW * kT;
+#ifndef PW
+#define PW 8
+#define PT 8
+#define PB 2
+#define BW 8
+#define BT 4
+#define BB 3
+#endif
 constexpr int kCh = 64;  // channels a CTA
 constexpr int kMaxRanks = 8;
 
@@ -206,16 +147,20 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool v
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+template <int CW>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void wait_async() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's share of a warp's copies of 8 token rows of 64 channels from c0 on.  CW: bytes a
+// A lane's share of a warp's copies of kT token rows of 64 channels from c0 on.  CW: bytes a
 // copy (16 or 4), or 0 for element loads.  The pointer follows the warp's rows from tile to
 // tile; rows outside [lo, hi) and channels outside the array arrive as zeros.
-template <typename T, int CW>
+template <typename T, int CW, int kT>
 struct Rows {
   static constexpr int E = CW > 0 ? CW / (int)sizeof(T) : 1;  // elements a copy
   static constexpr int CPR = kCh / E;                         // copies a row
@@ -231,18 +176,26 @@ struct Rows {
   __device__ __forceinline__ void start(const T *base, int64_t t0, int64_t stride, int64_t c0, int lane) {
     p = base + (t0 + row(0, lane)) * stride + c0 + chan(0, lane);
   }
-  // channels: D - c0
-  __device__ __forceinline__ void fetch(T *dst, int lo, int hi, int64_t stride, int64_t channels, int lane) const {
+  __device__ __forceinline__ const T *from(int q, int64_t stride) const {
+    return p + (row(q, 0) - row(0, 0)) * stride + (chan(q, 0) - chan(0, 0));
+  }
+  // whole: every row and channel is there
+  __device__ __forceinline__ void fetch(T *dst, bool whole, int lo, int hi, int64_t stride, int64_t channels,
+                                        int lane) const {
     const uint32_t to = smem_addr(dst) + lane * E * (int)sizeof(T);
+    if (CW == 16 && whole) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) copy_async<16>(to + q * 32 * 16, from(q, stride));
+      return;
+    }
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       const int j = row(q, lane);
       const bool valid = j >= lo && j < hi && chan(q, lane) < channels;
-      const T *from = p + (row(q, 0) - row(0, 0)) * stride + (chan(q, 0) - chan(0, 0));
       if constexpr (CW == 0)
-        dst[q * 32 + lane] = valid ? *from : T(0.f);
+        dst[q * 32 + lane] = valid ? *from(q, stride) : T(0.f);
       else
-        copy_async<CW>(to + q * 32 * CW, from, valid);
+        copy_async<CW>(to + q * 32 * CW, from(q, stride), valid);
     }
   }
 };
@@ -281,55 +234,81 @@ __device__ __forceinline__ void store_rank(Link *p, uint32_t rank, Link v) {
 }
 
 // What the warps and ranks of a scan tell one another, by parity of the tile.
+template <int kW>
 struct Links {
+  Link carry[2][32];  // H: the state entering the tile
   Link warp[2][kW][32];
   Link rank[2][kMaxRanks][32];
-  Link carry[2][32];  // H: the state entering the tile
+};
+__device__ __forceinline__ Link load_link(const Link &l) {
+  const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&l);
+  return {{u.x}, {u.y}};
+}
+
+// The exchange of a tile, in two halves so that a warp has other work while it waits: `publish` gives its own
+// update away, `collect` returns the state that enters its tokens.  Every warp of every rank calls each once a tile.
+template <bool kCluster, int kW>
+struct Exchange {
+  Links<kW> &l;
+  int warp, lane, rank, ranks;
+  Link before;  // the warps before this one
+  __device__ __forceinline__ void prefix(int par) {
+    before = {both(1.f), both(0.f)};
+    for (int w = 0; w < warp; ++w) before = then(before, load_link(l.warp[par][w][lane]));
+  }
+  __device__ __forceinline__ void publish(int par, Link mine) {
+    l.warp[par][warp][lane] = mine;
+    if constexpr (kCluster) {
+      __syncthreads();
+      prefix(par);
+      if (warp == kW - 1) {
+        const Link all = then(before, mine);
+        for (int k = rank + 1; k < ranks; ++k) store_rank(&l.rank[par][rank][lane], k, all);
+      }
+      arrive_ranks(warp == kW - 1);
+    }
+  }
+  __device__ __forceinline__ f2 collect(int par) {
+    if constexpr (kCluster) {
+      wait_ranks();
+    } else {
+      __syncthreads();
+      prefix(par);
+    }
+    f2 h = l.carry[par][lane].H;
+    if constexpr (kCluster)
+      for (int k = 0; k < rank; ++k) {
+        const Link f = load_link(l.rank[par][k][lane]);
+        h = fma2(f.A, h, f.H);
+      }
+    return fma2(before.A, h, before.H);
+  }
+  // The state after the tile's last token, from the last warp of the last rank, for the next tile (not
+  // after the last one: a rank may have left by then).
+  __device__ __forceinline__ void leave(int par, f2 h) {
+    const Link v = {both(0.f), h};
+    if constexpr (kCluster)
+      for (int k = 0; k < ranks; ++k) store_rank(&l.carry[par ^ 1][lane], k, v);
+    else
+      l.carry[par ^ 1][lane] = v;
+  }
+  __device__ __forceinline__ bool last() const { return warp == kW - 1 && rank == ranks - 1; }
 };
 
-// The state entering this warp's tokens, given its own update `mine`; all ranks call it once a tile.  `meanwhile`
-// runs while the ranks wait for one another.
-template <bool kCluster, typename F>
-__device__ __forceinline__ f2 enter(Links &l, int par, int warp, int lane, int rank, int ranks, Link mine, F meanwhile) {
-  l.warp[par][warp][lane] = mine;
-  if constexpr (!kCluster) meanwhile();
-  __syncthreads();
-  Link before = {both(1.f), both(0.f)};
-  for (int w = 0; w < warp; ++w) before = then(before, l.warp[par][w][lane]);
-  if constexpr (kCluster) {
-    if (warp == kW - 1) {
-      const Link all = then(before, mine);
-      for (int k = rank + 1; k < ranks; ++k) store_rank(&l.rank[par][rank][lane], k, all);
-    }
-    arrive_ranks(warp == kW - 1);
-    meanwhile();
-    wait_ranks();
-  }
-  f2 h = l.carry[par][lane].H;
-  if constexpr (kCluster)
-    for (int k = 0; k < rank; ++k) h = fma2(l.rank[par][k][lane].A, h, l.rank[par][k][lane].H);
-  return fma2(before.A, h, before.H);
-}
-// The state after the tile's last token, from the last warp of the last rank, for the next tile (not
-// after the last one: a rank may have left by then).
-template <bool kCluster>
-__device__ __forceinline__ void leave(Links &l, int par, int lane, int ranks, f2 h) {
-  const Link v = {both(0.f), h};
-  if constexpr (kCluster)
-    for (int k = 0; k < ranks; ++k) store_rank(&l.carry[par ^ 1][lane], k, v);
-  else
-    l.carry[par ^ 1][lane] = v;
-}
-
-template <typename T, int N>
+template <typename T, int N, int kW, int kT>
 struct ScanSmem {
   T in[kW][2][N][kT][kCh];
-  Links links;
+  Links<kW> links;  // the last member: without a cluster its `rank` is not allocated
 };
+template <typename T, int N, int kW, int kT>
+size_t scan_smem(int ranks) {
+  return sizeof(ScanSmem<T, N, kW, kT>) - (ranks > 1 ? 0 : sizeof(Links<kW>::rank));
+}
 
 // A CTA's place in the grid.
 struct Place {
   int warp, lane, rank, ranks, n;  // n: channels of this lane
+  bool whole;                      // all 64 channels are there
   int64_t b, c0, c;
 };
 template <bool kCluster>
@@ -344,34 +323,53 @@ __device__ __forceinline__ Place place(int64_t D, int blocks) {
   p.c0 = (int64_t)(blk % blocks) * kCh;
   p.c = p.c0 + 2 * p.lane;
   p.n = (int)max((int64_t)0, min((int64_t)2, D - p.c));
+  p.whole = D - p.c0 >= kCh;
   return p;
 }
 
-template <typename T, int CW, bool kCluster>
-__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 3 : 2)
+template <typename T, int CW, bool kCluster, int kW, int kT>
+__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? PB : (PB + 1) / 2)
     k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                   const float *__restrict__ A, const float *init, T *__restrict__ h, float *final_state, GlrDims d,
                   int blocks) {
+  constexpr int kTile = kW * kT;
   extern __shared__ __align__(16) char raw[];
-  ScanSmem<T, 3> &sm = *reinterpret_cast<ScanSmem<T, 3> *>(raw);
+  ScanSmem<T, 3, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 3, kW, kT> *>(raw);
   const Place p = place<kCluster>(d.D, blocks);
+  Exchange<kCluster, kW> ex{sm.links, p.warp, p.lane, p.rank, p.ranks, {}};
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
   const int64_t t0 = p.rank * kTile + p.warp * kT;  // this warp's first token
   int64_t left = d.L - t0;                          // tokens from it to the end
-  Rows<T, CW> rows[3];
+  Rows<T, CW, kT> rows[3];
   rows[0].start(x + p.b * d.L * d.row, t0, d.row, p.c0, p.lane);
   rows[1].start(r + p.b * d.L * d.row, t0, d.row, p.c0, p.lane);
   rows[2].start(i + p.b * d.L * d.row, t0, d.row, p.c0, p.lane);
   auto load = [&](int stage, int64_t rest) {  // rest: tokens of the sequence from the first row on
     if (rest > 0) {
+      const bool whole = p.whole && rest >= kT;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], 0, (int)min(rest, (int64_t)kT), d.row, d.D - p.c0, p.lane);
+        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], whole, 0, (int)min(rest, (int64_t)kT), d.row, d.D - p.c0, p.lane);
         rows[k].p += step * d.row;
       }
     }
     commit_async();
+  };
+  // the gates of the tile in `stage`, of which the sequence has `rest` tokens
+  auto gates = [&](int stage, int64_t rest, f2 (&a)[kT], f2 (&v)[kT]) {
+    wait_async<1>();
+    __syncwarp();
+    const auto &in = sm.in[p.warp][stage];
+#pragma unroll
+    for (int j = 0; j < kT; ++j)
+      gate(load2(&in[0][j][2 * p.lane]), load2(&in[1][j][2 * p.lane]), load2(&in[2][j][2 * p.lane]), Ac, a[j], v[j]);
+    if (rest < kT) {  // the sequence ends within these tokens: the rest leave the state as it is
+#pragma unroll
+      for (int j = 0; j < kT; ++j)
+        if (j >= rest) a[j] = both(1.f), v[j] = both(0.f);
+    }
+    __syncwarp();
   };
   load(0, left);
   load(1, left - step);
@@ -384,32 +382,30 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 3 : 2)
   f2 s = both(0.f);
   for (int64_t tile = 0; tile < tiles; ++tile, left -= step, out += step * d.D) {
     const int par = tile & 1;
-    wait_async<1>();
-    __syncwarp();
     f2 a[kT], v[kT];
-    const auto &in = sm.in[p.warp][par];
-#pragma unroll
-    for (int j = 0; j < kT; ++j)
-      gate(load2(&in[0][j][2 * p.lane]), load2(&in[1][j][2 * p.lane]), load2(&in[2][j][2 * p.lane]), Ac, a[j], v[j]);
-    if (left < kT) {  // the sequence ends within these tokens: the rest leave the state as it is
-#pragma unroll
-      for (int j = 0; j < kT; ++j)
-        if (j >= left) a[j] = both(1.f), v[j] = both(0.f);
-    }
+    gates(par, left, a, v);
     Link all = {a[0], v[0]};
 #pragma unroll
     for (int j = 1; j < kT; ++j) all = then(all, {a[j], v[j]});
-    __syncwarp();
-    s = enter<kCluster>(sm.links, par, p.warp, p.lane, p.rank, p.ranks, all, [&] { load(par, left - 2 * step); });
+    load(par, left - 2 * step);
+    ex.publish(par, all);
+    s = ex.collect(par);
+    if (left >= kT) {
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
-      s = fma2(a[j], s, v[j]);
-      if (j < left) store2<CW == 16>(out + j * d.D, s, p.n);
+      for (int j = 0; j < kT; ++j) {
+        s = fma2(a[j], s, v[j]);
+        store2<CW == 16>(out + j * d.D, s, p.n);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kT; ++j) {
+        s = fma2(a[j], s, v[j]);
+        if (j < left) store2<CW == 16>(out + j * d.D, s, p.n);
+      }
     }
-    if (p.warp == kW - 1 && p.rank == p.ranks - 1 && tile + 1 < tiles)
-      leave<kCluster>(sm.links, par, p.lane, p.ranks, s);
+    if (ex.last() && tile + 1 < tiles) ex.leave(par, s);
   }
-  if (p.warp == kW - 1 && p.rank == p.ranks - 1) store2<false>(final_state + p.b * d.D + p.c, s, p.n);
+  if (ex.last()) store2<false>(final_state + p.b * d.D + p.c, s, p.n);
 }
 
 template <typename T>
@@ -431,20 +427,22 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
 // tiles from the sequence's end.  Of the gates only the decay is needed before the barrier; it is kept,
 // and the rest is formed when g is known.  A tile is 5 inputs deep, which leaves two CTAs an SM for bf16
 // and one for fp32.
-template <typename T, int CW, bool kCluster>
-__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
+template <typename T, int CW, bool kCluster, int kW, int kT>
+__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? BB : (BB + 1) / 2)
     k_glr_backward(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                    const float *__restrict__ A, const float *__restrict__ init, const T *__restrict__ h,
                    const T *__restrict__ dh, const float *dfinal, T *__restrict__ dx, T *__restrict__ dr,
                    T *__restrict__ di, float *dinit, float *__restrict__ part, GlrDims d, int blocks) {
+  constexpr int kTile = kW * kT;
   extern __shared__ __align__(16) char raw[];
-  ScanSmem<T, 5> &sm = *reinterpret_cast<ScanSmem<T, 5> *>(raw);
+  ScanSmem<T, 5, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 5, kW, kT> *>(raw);
   const Place p = place<kCluster>(d.D, blocks);
+  Exchange<kCluster, kW> ex{sm.links, p.warp, p.lane, p.rank, p.ranks, {}};
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
   // this warp's tokens are t .. t + 7; those below 0 lie before the sequence
   int64_t t = d.L - kT - (p.rank * kTile + p.warp * kT);
-  Rows<T, CW> rows[5];  // r, dh, i, x, h_{t-1}
+  Rows<T, CW, kT> rows[5];  // r, dh, i, x, h_{t-1}
   const int64_t at = p.b * d.L * d.row, o = p.b * d.L * d.D;
   rows[0].start(r + at, t, d.row, p.c0, p.lane);
   rows[1].start(dh + o, t, d.D, p.c0, p.lane);
@@ -453,11 +451,12 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
   rows[4].start(h + o, t - 1, d.D, p.c0, p.lane);
   auto load = [&](int stage, int64_t t) {
     if (t > -kT) {
+      const bool whole = p.whole && t > 0;
 #pragma unroll
       for (int k = 0; k < 5; ++k) {
         const int64_t stride = k == 1 || k == 4 ? d.D : d.row;
         const int lo = (int)max((int64_t)0, (k == 4 ? 1 : 0) - t);
-        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], lo, kT, stride, d.D - p.c0, p.lane);
+        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], whole, lo, kT, stride, d.D - p.c0, p.lane);
         rows[k].p -= step * stride;
       }
     }
@@ -492,7 +491,8 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
       for (int j = kT - 1; j >= 0; --j) all = then(all, {a[j], a[j] * load2(&in[1][j][2 * p.lane])});
     }
-    s = enter<kCluster>(sm.links, par, p.warp, p.lane, p.rank, p.ranks, all, [] {});
+    ex.publish(par, all);
+    s = ex.collect(par);
 #pragma unroll
     for (int j = kT - 1; j >= 0; --j) {
       if (!any) break;
@@ -509,10 +509,9 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? 2 : 1)
     }
     __syncwarp();
     load(par, t - 2 * step);
-    if (p.warp == kW - 1 && p.rank == p.ranks - 1 && tile + 1 < tiles)
-      leave<kCluster>(sm.links, par, p.lane, p.ranks, s);
+    if (ex.last() && tile + 1 < tiles) ex.leave(par, s);
   }
-  if (dinit != nullptr && p.warp == kW - 1 && p.rank == p.ranks - 1) store2<false>(dinit + p.b * d.D + p.c, s, p.n);
+  if (dinit != nullptr && ex.last()) store2<false>(dinit + p.b * d.D + p.c, s, p.n);
   // dA over the CTA's warps, in order
   wait_async<0>();
   __syncthreads();
@@ -539,18 +538,20 @@ bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // CTAs that share a sequence: as many as the GPU holds at once (`resident` an SM) and the
 // sequence has tiles for.
-int pick_ranks(int64_t ctas, int64_t L, int resident) {
-  const int64_t room = (int64_t)148 * resident / ctas, tiles = (L + kTile - 1) / kTile;
+int pick_ranks(int64_t ctas, int64_t L, int tile, int resident) {
+  if (const char *e = getenv("RANKS")) return std::max(1, std::min(atoi(e), (int)((L + tile - 1) / tile)));
+  const int64_t room = (int64_t)148 * resident / ctas, tiles = (L + tile - 1) / tile;
   return (int)std::max<int64_t>(1, std::min<int64_t>({room, tiles, kMaxRanks}));
 }
 
 template <typename... P, typename... V>
-cudaError_t launch_ranks(void (*f)(P...), int64_t ctas, int ranks, size_t smem, cudaStream_t st, V... v) {
+cudaError_t launch_ranks(void (*f)(P...), int64_t ctas, int ranks, int warps, size_t smem, cudaStream_t st,
+                         V... v) {
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(ctas * ranks));
-  cfg.blockDim = dim3(kW * 32);
+  cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -569,14 +570,15 @@ cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *
   const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
   constexpr int E = 16 / sizeof(T);
   const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && d.D % E == 0 && d.row % E == 0;
-  const int ranks = pick_ranks(ctas, d.L, sizeof(T) == 2 ? 3 : 1);
+  constexpr int W = PW, N = PT;
+  const int ranks = pick_ranks(ctas, d.L, W * N, sizeof(T) == 2 ? PB : (PB + 1) / 2);
   auto run = [&](auto *one, auto *many) {
-    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, sizeof(ScanSmem<T, 3>), st, x, r, i, A, init, h,
+    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, W, scan_smem<T, 3, W, N>(ranks), st, x, r, i, A, init, h,
                         final_state, d, (int)blocks);
   };
-  if (w16) return run(k_glr_prefill<T, 16, false>, k_glr_prefill<T, 16, true>);
+  if (w16) return run(k_glr_prefill<T, 16, false, W, N>, k_glr_prefill<T, 16, true, W, N>);
   constexpr int CW = sizeof(T) == 4 ? 4 : 0;
-  return run(k_glr_prefill<T, CW, false>, k_glr_prefill<T, CW, true>);
+  return run(k_glr_prefill<T, CW, false, W, N>, k_glr_prefill<T, CW, true, W, N>);
 }
 
 template <typename T>
@@ -597,14 +599,15 @@ cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float 
   constexpr int E = 16 / sizeof(T);
   const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && wide(dh) && wide(dx) && wide(dr) && wide(di) &&
                    d.D % E == 0 && d.row % E == 0 && d.grad % E == 0;
-  const int ranks = pick_ranks(ctas, d.L, sizeof(T) == 2 ? 2 : 1);
+  constexpr int W = BW, N = BT;
+  const int ranks = pick_ranks(ctas, d.L, W * N, sizeof(T) == 2 ? BB : (BB + 1) / 2);
   auto run = [&](auto *one, auto *many) {
-    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, sizeof(ScanSmem<T, 5>), st, x, r, i, A, init, h, dh,
+    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, W, scan_smem<T, 5, W, N>(ranks), st, x, r, i, A, init, h, dh,
                         dfinal, dx, dr, di, dinit, part, d, (int)blocks);
   };
   constexpr int CW = sizeof(T) == 4 ? 4 : 0;
-  cudaError_t e = w16 ? run(k_glr_backward<T, 16, false>, k_glr_backward<T, 16, true>)
-                      : run(k_glr_backward<T, CW, false>, k_glr_backward<T, CW, true>);
+  cudaError_t e = w16 ? run(k_glr_backward<T, 16, false, W, N>, k_glr_backward<T, 16, true, W, N>)
+                      : run(k_glr_backward<T, CW, false, W, N>, k_glr_backward<T, CW, true, W, N>);
   if (e != cudaSuccess) return e;
   k_glr_sum<<<(unsigned)((d.D + 127) / 128), 128, 0, st>>>(part, dA, d.D, d.b * ranks);
   return cudaGetLastError();

@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 
 namespace ssd {
@@ -13,10 +14,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kParts = 592;  // most rows of partial sums
-
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
@@ -70,123 +67,166 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Rows in registers.  A unit (one group of one row) belongs to `tpr` threads: a power of two up
-// to a warp, with several units a CTA, or a whole CTA of tpr threads.  A thread holds NV runs of
-// VEC neighbouring channels, so the row is read once, with 16-byte loads where the arrays allow.
-template <int VEC, typename T>
-__device__ __forceinline__ void load_run(const T *p, float (&v)[VEC]) {
-  if constexpr (VEC == 8 && sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+// to a warp, with several units a CTA, or whole warps.  A thread holds NV runs of VEC neighbouring
+// channels, run k at (k tpr + lane) VEC, so the row is read once, with 16-byte loads where the
+// arrays allow (VEC = 1: element loads).  All loads are issued before the first use; runs past the
+// unit's end are loaded from its start and set to zero.
+// Most threads of a CTA whose threads hold n channels each.
+constexpr int row_threads(int n) { return n > 16 ? 512 : 1024; }
+
+template <typename T, int VEC, int NV>
+struct Runs {
+  static constexpr int kPieces = VEC > 1 ? VEC * (int)sizeof(T) / 16 : 1;  // 16-byte pieces a run
+  using Piece = std::conditional_t<(VEC > 1), uint4, T>;
+  Piece q[NV][kPieces];
+
+  // from memory: run k at p + at[k]
+  __device__ __forceinline__ void load(const T *p, const int (&at)[NV]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(q[k] << 16);
-      v[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
-    }
-  } else if constexpr (VEC % 4 == 0) {
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-      const float4 u = load4(p + k);
-      v[k] = u.x, v[k + 1] = u.y, v[k + 2] = u.z, v[k + 3] = u.w;
-    }
-  } else {
-    v[0] = to_f32(p[0]);
+      for (int j = 0; j < kPieces; ++j) q[k][j] = reinterpret_cast<const Piece *>(p + at[k])[j];
   }
-}
-template <int VEC, typename T>
-__device__ __forceinline__ void store_run(T *p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8 && sizeof(T) == 2) {
-    uint4 u;
-    uint32_t *q = &u.x;
+  // from the thread's pieces in shared memory, `pitch` apart; those of a run begin `run` pieces after the last one's
+  __device__ __forceinline__ void load_pieces(const uint4 *from, int run, int pitch) {
+    if constexpr (VEC > 1)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-      q[k] = *reinterpret_cast<const uint32_t *>(&b);
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) q[k][j] = from[(k * run + j) * pitch];
+  }
+  // the thread's channels 2 e and 2 e + 1, in the order of its runs
+  __device__ __forceinline__ f2 operator[](int e) const {
+    if constexpr (VEC == 1) {
+      return mk(to_f32(q[2 * e][0]), to_f32(q[2 * e + 1][0]));
+    } else {
+      const int k = 2 * e / VEC, c = 2 * e % VEC, per = 16 / (int)sizeof(T);
+      const uint4 &u = q[k][c / per];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      if constexpr (sizeof(T) == 2)
+        return from_bf16x2(w[c % per / 2]);
+      else
+        return mk(__uint_as_float(w[c % per]), __uint_as_float(w[c % per + 1]));
     }
-    *reinterpret_cast<uint4 *>(p) = u;
-  } else if constexpr (VEC % 4 == 0) {
+  }
+};
+
+// Out again, rounded; run k at p + at[k] where on[k].
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_runs(T *p, const int (&at)[NV], const bool (&on)[NV], const f2 (&v)[NV * VEC / 2]) {
 #pragma unroll
-    for (int k = 0; k < VEC; k += 4) *reinterpret_cast<float4 *>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-  } else {
-    p[0] = from_f32<T>(v[0]);
+  for (int k = 0; k < NV; ++k) {
+    if (!on[k]) continue;
+    if constexpr (VEC == 1) {
+      const float2 s = split(v[k / 2]);
+      p[at[k]] = from_f32<T>(k % 2 ? s.y : s.x);
+    } else if constexpr (sizeof(T) == 2) {
+      const f2 *e = &v[k * VEC / 2];
+      *reinterpret_cast<uint4 *>(p + at[k]) =
+          make_uint4(to_bf16x2(e[0]), to_bf16x2(e[1]), to_bf16x2(e[2]), to_bf16x2(e[3]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; c += 4) {
+        const float2 a = split(v[(k * VEC + c) / 2]), b = split(v[(k * VEC + c) / 2 + 1]);
+        *reinterpret_cast<float4 *>(p + at[k] + c) = make_float4(a.x, a.y, b.x, b.y);
+      }
+    }
   }
 }
 
-// Sums over a unit's threads, in every one of them; all of the CTA's threads call it.  sh: N floats a warp.
-template <int N>
-__device__ __forceinline__ void unit_sum(float (&v)[N], int tpr, float *sh) {
-  for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1)
+template <int VEC, int NV>
+__device__ __forceinline__ void zero_off(f2 (&v)[NV * VEC / 2], const bool (&on)[NV]) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (tpr <= 32) return;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int k = 0; k < N; ++k) sh[(threadIdx.x >> 5) * N + k] = v[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 0.f;
-  const int first = threadIdx.x / tpr * (tpr >> 5);
-  for (int j = first; j < first + (tpr >> 5); ++j)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += sh[j * N + k];
+  for (int e = 0; e < NV * VEC / 2; ++e) {
+    const float2 s = split(v[e]);
+    v[e] = mk(on[2 * e / VEC] ? s.x : 0.f, on[(2 * e + 1) / VEC] ? s.y : 0.f);
+  }
+}
+
+__device__ __forceinline__ float total(f2 v) {
+  const float2 s = split(v);
+  return s.x + s.y;
+}
+
+// A sum (or a pair of them) over a unit's threads, in every one of them.  Units of several warps meet at a barrier of
+// their own; sh: one a warp of the CTA, not used by the call before (two buffers in turn).
+__device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ f2 from_lane(f2 v, int o) { return {__shfl_xor_sync(0xffffffffu, v.v, o)}; }
+template <typename S>
+__device__ __forceinline__ S unit_sum(S v, int tpr, S *sh) {
+  for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) v = v + from_lane(v, o);
+  if (tpr <= 32) return v;
+  const int warp = threadIdx.x >> 5, warps = tpr >> 5, unit = threadIdx.x / tpr;
+  if ((threadIdx.x & 31) == 0) sh[warp] = v;
+  if (tpr == blockDim.x)
+    __syncthreads();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(unit + 1), "r"(tpr) : "memory");
+  v = sh[unit * warps];
+#pragma unroll 4
+  for (int j = 1; j < warps; ++j) v = v + sh[unit * warps + j];
+  return v;
 }
 
 template <Mode M, typename TX, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(row_threads(NV *VEC))
     k_norm_rows(const TX *x, const float *__restrict__ scale, const TR *wide, const float *__restrict__ w, float eps,
                 TR *wide_out, TX *out, NormDims d, int tpr, int W) {
   __shared__ float sh[32];
+  constexpr int E = NV * VEC / 2;
   const int lane = threadIdx.x % tpr;
   const int64_t unit = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
   const bool live = unit < d.rows * d.G;
   const int64_t row = live ? unit / d.G : 0;
   const int c0 = (int)(live ? unit % d.G : 0) * W;
-  const TX *xr = x + row * (M == kResidual ? d.D : d.gate) + c0;
-  const TR *wr = wide + row * d.D + c0;
-  float v[NV][VEC], gate[M == kNormFirst ? NV : 1][VEC], ss[1] = {0.f};
+  int at[NV];
+  bool on[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (k * tpr + lane) * VEC;
-    if (!live || c >= W) continue;
-    float a[VEC], b[VEC];
-    load_run<VEC>(xr + c, a);
-    if (M != kResidual || wide != nullptr) load_run<VEC>(wr + c, b);
-    if (M == kResidual) {
-      if (scale != nullptr) {
-        float sc[VEC];
-        load_run<VEC>(scale + c, sc);
+    at[k] = (k * tpr + lane) * VEC;
+    on[k] = live && at[k] < W;
+    if (!on[k]) at[k] = 0;
+  }
+  Runs<TX, VEC, NV> rx;
+  Runs<TR, VEC, NV> rw;
+  rx.load(x + row * (M == kResidual ? d.D : d.gate) + c0, at);
+  if (M != kResidual || wide != nullptr) rw.load(wide + row * d.D + c0, at);
+  f2 v[E], gate[M == kNormFirst ? E : 1];
+  if (M == kResidual) {
+    if (scale != nullptr) {
+      Runs<float, VEC, NV> rs;
+      rs.load(scale, at);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) a[e] *= sc[e];
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[k][e] = wide != nullptr ? a[e] + b[e] : a[e];
+      for (int e = 0; e < E; ++e) v[e] = rx[e] * rs[e];
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float g = a[e] * sigmoid(a[e]);
-        v[k][e] = M == kGateFirst ? b[e] * g : b[e];
-        if (M == kNormFirst) gate[k][e] = g;
-      }
+      for (int e = 0; e < E; ++e) v[e] = rx[e];
     }
+    if (wide != nullptr)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) ss[0] = fmaf(v[k][e], v[k][e], ss[0]);
-  }
-  unit_sum(ss, tpr, sh);
-  const float rstd = rsqrtf(ss[0] / (float)W + eps);
+      for (int e = 0; e < E; ++e) v[e] = v[e] + rw[e];
+  } else {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (k * tpr + lane) * VEC;
-    if (!live || c >= W) continue;
-    if (M == kResidual && wide_out != nullptr) store_run<VEC>(wide_out + row * d.D + c0 + c, v[k]);
-    float o[VEC];
-    load_run<VEC>(w + c0 + c, o);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      o[e] *= v[k][e] * rstd;
-      if (M == kNormFirst) o[e] *= gate[k][e];
+    for (int e = 0; e < E; ++e) {
+      const f2 z = rx[e], g = z * sigmoid(z);
+      v[e] = M == kGateFirst ? rw[e] * g : rw[e];
+      if (M == kNormFirst) gate[e] = g;
     }
-    store_run<VEC>(out + row * d.D + c0 + c, o);
   }
+  if (!on[NV - 1]) zero_off<VEC, NV>(v, on);
+  f2 ss = both(0.f);
+#pragma unroll
+  for (int e = 0; e < E; ++e) ss = fma2(v[e], v[e], ss);
+  const f2 rstd = both(rsqrtf(unit_sum(total(ss), tpr, sh) / (float)W + eps));
+  if (M == kResidual && wide_out != nullptr) store_runs<TR, VEC, NV>(wide_out + row * d.D + c0, at, on, v);
+  Runs<float, VEC, NV> rg;
+  rg.load(w + c0, at);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    v[e] = v[e] * rstd * rg[e];
+    if (M == kNormFirst) v[e] = v[e] * gate[e];
+  }
+  store_runs<TX, VEC, NV>(out + row * d.D + c0, at, on, v);
 }
 
 // Gradients of rows too long for registers.  A CTA takes rows blockIdx.x, + gridDim.x, ...; a column belongs to one thread of it, which adds the
@@ -270,189 +310,231 @@ __device__ __forceinline__ void wait_async(int left) {  // at most `left` (0 .. 
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory, all its CTAs together
+#ifndef EPT
+#define EPT 8
+#define T8 640
+#define RES 640
+#define RB 216
+#endif
+constexpr int kRingBytes = RB * 1024;  // of an SM's shared memory, all its CTAs together
 
-// 16-byte pieces of a run of VEC channels of the four inputs
+// 16-byte pieces of a run of VEC channels of the four inputs, and of an fp32 vector
 template <Mode M, typename TX, typename TR, int VEC>
 struct Pieces {
-  static constexpr int kX = VEC * (int)sizeof(TX) / 16, kR = VEC * (int)sizeof(TR) / 16;
-  static constexpr int wide = 0, dout = kR, x = kR + kX, dwide = kR + 2 * kX;
-  static constexpr int all = M == kResidual ? 2 * kR + 2 * kX : kR + 2 * kX;
+  enum : int {
+    kX = VEC * (int)sizeof(TX) / 16, kR = VEC * (int)sizeof(TR) / 16, kF = VEC / 4,
+    wide = 0, dout = kR, x = kR + kX, dwide = kR + 2 * kX,  // where each input's pieces begin
+    all = M == kResidual ? 2 * kR + 2 * kX : kR + 2 * kX
+  };
 };
 
 template <Mode M, typename TX, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(VEC *NV == 8 ? 640 : 512)
+__global__ void __launch_bounds__(640)
     k_norm_backward_rows(const TX *__restrict__ x, const float *__restrict__ scale, const TR *__restrict__ wide,
                          const float *__restrict__ w, float eps, const TX *__restrict__ dout, const TR *dwide, TX *dx,
                          TR *dwide_out, float *__restrict__ pw, float *__restrict__ ps, NormDims d, int tpr, int W,
                          int parts, int stages) {
   extern __shared__ __align__(16) char raw[];
-  __shared__ float sh[2 * 32];
+  __shared__ f2 sh[2][32];
   using P = Pieces<M, TX, TR, VEC>;
+  constexpr int E = NV * VEC / 2;
   const int lane = threadIdx.x % tpr, sub = threadIdx.x / tpr, subs = blockDim.x / tpr;
   const int part = blockIdx.x % parts, c0 = blockIdx.x / parts * W;
   const int64_t step = (int64_t)parts * subs, first = (int64_t)part * subs;
   const int64_t turns = (d.rows - first + step - 1) / step;  // the same for all of the CTA
   const int64_t xs = M == kResidual ? d.D : d.gate;
   const bool want_x = M != kResidual || ps != nullptr, want_d = M == kResidual && dwide != nullptr;
+  int at[NV];
+  bool in[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    at[k] = (k * tpr + lane) * VEC;
+    in[k] = at[k] < W;
+    if (!in[k]) at[k] = 0;
+  }
+  // a thread's pieces lie blockDim.x apart, so that a warp's accesses are contiguous
+  const int pitch = blockDim.x, stage_pitch = NV * P::all * pitch;
+  const bool scaled = M == kResidual && scale != nullptr;
   uint4 *ring = reinterpret_cast<uint4 *>(raw) + threadIdx.x;
-  auto slot = [&](int stage, int k, int piece) { return ring + ((stage * NV + k) * P::all + piece) * blockDim.x; };
+  uint4 *mine = ring + stages * stage_pitch;  // this thread's weights (and scales), behind the ring
   auto fetch = [&](int64_t turn, int stage) {
     if constexpr (VEC > 1) {
       const int64_t row = first + turn * step + sub;
-      if (turn < turns && row < d.rows)
+      if (turn < turns && row < d.rows) {
+        const int64_t o = row * d.D + c0;
+        uint4 *slot = ring + stage * stage_pitch;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-          const int c = (k * tpr + lane) * VEC;
-          if (c >= W) continue;
-          const int64_t o = row * d.D + c0 + c;
+          uint4 *to = slot + k * P::all * pitch;
 #pragma unroll
           for (int q = 0; q < P::kR; ++q) {
-            copy16(slot(stage, k, P::wide + q), reinterpret_cast<const uint4 *>(wide + o) + q);
-            if (want_d) copy16(slot(stage, k, P::dwide + q), reinterpret_cast<const uint4 *>(dwide + o) + q);
+            copy16(to + (P::wide + q) * pitch, reinterpret_cast<const uint4 *>(wide + o + at[k]) + q);
+            if (want_d) copy16(to + (P::dwide + q) * pitch, reinterpret_cast<const uint4 *>(dwide + o + at[k]) + q);
           }
 #pragma unroll
           for (int q = 0; q < P::kX; ++q) {
-            copy16(slot(stage, k, P::dout + q), reinterpret_cast<const uint4 *>(dout + o) + q);
-            if (want_x) copy16(slot(stage, k, P::x + q), reinterpret_cast<const uint4 *>(x + row * xs + c0 + c) + q);
+            copy16(to + (P::dout + q) * pitch, reinterpret_cast<const uint4 *>(dout + o + at[k]) + q);
+            if (want_x)
+              copy16(to + (P::x + q) * pitch, reinterpret_cast<const uint4 *>(x + row * xs + c0 + at[k]) + q);
           }
         }
+      }
       commit_async();
     }
   };
-  // a run of one input, from the ring or from memory
-  auto read = [&](int stage, int k, int piece, const auto *p, float (&v)[VEC]) {
-    using T = std::remove_cv_t<std::remove_pointer_t<decltype(p)>>;
-    if constexpr (VEC > 1) {
-      constexpr int E = 16 / (int)sizeof(T);
+  if constexpr (VEC > 1)
 #pragma unroll
-      for (int q = 0; q < VEC / E; ++q) {
-        float part[E];
-        load_run<E>(reinterpret_cast<const T *>(slot(stage, k, piece + q)), part);
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[q * E + e] = part[e];
+      for (int q = 0; q < P::kF; ++q) {
+        mine[(k * P::kF + q) * pitch] = reinterpret_cast<const uint4 *>(w + c0 + at[k])[q];
+        if (scaled) mine[((NV + k) * P::kF + q) * pitch] = reinterpret_cast<const uint4 *>(scale + at[k])[q];
       }
-    } else {
-      load_run<VEC>(p, v);
-    }
-  };
-  float sw[NV][VEC], ss[M == kResidual ? NV : 1][VEC];
+  f2 sw[E], ss[M == kResidual ? E : 1];
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      sw[k][e] = 0.f;
-      if (M == kResidual) ss[k][e] = 0.f;
-    }
+  for (int e = 0; e < E; ++e) {
+    sw[e] = both(0.f);
+    if (M == kResidual) ss[e] = both(0.f);
+  }
   for (int s = 0; s < stages; ++s) fetch(s, s);
   int stage = 0;
   for (int64_t turn = 0; turn < turns; ++turn) {
-    const int64_t row = first + turn * step + sub, o = row * d.D + c0;
+    const int64_t row = first + turn * step + sub;
     const bool live = row < d.rows;
-    if (VEC > 1) wait_async(stages - 1);
-    // what is normed, the gradient of the weighted norm, its product with the weight, and the other inputs
-    float v[NV][VEC], un[NV][VEC], uw[NV][VEC], other[NV][VEC], more[NV][VEC], sums[2] = {0.f, 0.f};
+    bool on[NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (k * tpr + lane) * VEC;
-      if (!live || c >= W) continue;
-      read(stage, k, P::wide, wide + o + c, v[k]);
-      read(stage, k, P::dout, dout + o + c, un[k]);
-      if (want_x) read(stage, k, P::x, x + row * xs + c0 + c, other[k]);
-      if (want_d) read(stage, k, P::dwide, dwide + o + c, more[k]);
-      load_run<VEC>(w + c0 + c, uw[k]);
+    for (int k = 0; k < NV; ++k) on[k] = live && in[k];
+    if constexpr (VEC > 1) wait_async(stages - 1);
+    const uint4 *slot = ring + stage * stage_pitch;
+    // a run of an input: from its slot, each time it is needed, or from memory
+    auto weight = [&](auto &runs, int vector, const float *p) {
+      if constexpr (VEC > 1) runs.load_pieces(mine + vector * NV * P::kF * pitch, P::kF, pitch);
+      else runs.load(p, at);
+    };
+    auto take = [&](auto &runs, int piece, const auto *p) {
+      if constexpr (VEC > 1) runs.load_pieces(slot + piece * pitch, P::all, pitch);
+      else runs.load(p, at);
+    };
+    const int64_t r = live ? row : 0, ro = r * d.D + c0;
+    // v: what is normed; uw: the gradient of the weighted norm times the weight
+    f2 v[E], uw[E], s0 = both(0.f), s1 = both(0.f);
+    {
+      Runs<TR, VEC, NV> rwide;
+      Runs<TX, VEC, NV> rdout, rx;
+      Runs<float, VEC, NV> rg;
+      take(rwide, P::wide, wide + ro);
+      take(rdout, P::dout, dout + ro);
+      if (M != kResidual) take(rx, P::x, x + r * xs + c0);
+      weight(rg, 0, w + c0);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (M == kGateFirst) {
-          more[k][e] = v[k][e];  // y
-          v[k][e] *= other[k][e] * sigmoid(other[k][e]);
+      for (int e = 0; e < E; ++e) {
+        v[e] = rwide[e];
+        uw[e] = rdout[e] * rg[e];
+        if (M != kResidual) {
+          const f2 z = rx[e], g = z * sigmoid(z);
+          if (M == kGateFirst) v[e] = v[e] * g;
+          if (M == kNormFirst) uw[e] = uw[e] * g;
         }
-        if (M == kNormFirst) {
-          more[k][e] = un[k][e];  // dout
-          un[k][e] *= other[k][e] * sigmoid(other[k][e]);
-        }
-        uw[k][e] *= un[k][e];
-        sums[0] = fmaf(v[k][e], v[k][e], sums[0]);
-        sums[1] = fmaf(uw[k][e], v[k][e], sums[1]);
       }
+    }
+    if (!on[NV - 1]) {
+      zero_off<VEC, NV>(v, on);
+      zero_off<VEC, NV>(uw, on);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      s0 = fma2(v[e], v[e], s0);
+      s1 = fma2(uw[e], v[e], s1);
+    }
+    const float2 sums = split(unit_sum(mk(total(s0), total(s1)), tpr, sh[turn & 1]));
+    if (live) {  // nothing was fetched for a row past the last one
+      const float rs1 = rsqrtf(sums.x / (float)W + eps);
+      const f2 rstd = both(rs1), mean = both(-sums.y * rs1 / (float)W);
+      Runs<TX, VEC, NV> rdout, rx;
+      f2 a[E];
+      take(rdout, P::dout, dout + ro);
+      if (want_x) take(rx, P::x, x + r * xs + c0);
+      if (M == kResidual) {
+        Runs<float, VEC, NV> rs;
+        Runs<TR, VEC, NV> rd;
+        if (want_d) take(rd, P::dwide, dwide + ro);
+        if (scaled) weight(rs, 1, scale);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const f2 n = v[e] * rstd;
+          f2 dv = rstd * fma2(n, mean, uw[e]);
+          sw[e] = fma2(rdout[e], n, sw[e]);
+          if (want_d) dv = dv + rd[e];
+          if (ps != nullptr) ss[e] = fma2(dv, rx[e], ss[e]);
+          a[e] = scaled ? dv * rs[e] : dv;
+          v[e] = dv;
+        }
+      } else {
+        Runs<TR, VEC, NV> ry;
+        Runs<float, VEC, NV> rg;
+        if (M == kGateFirst) take(ry, P::wide, wide + ro);
+        if (M == kNormFirst) weight(rg, 0, w + c0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const f2 n = v[e] * rstd, z = rx[e], sg = sigmoid(z), g = z * sg;
+          const f2 dv = rstd * fma2(n, mean, uw[e]), slope = fma2(g, fma2(sg, both(-1.f), both(1.f)), sg);
+          if (M == kGateFirst) {
+            sw[e] = fma2(rdout[e], n, sw[e]);
+            a[e] = dv * ry[e] * slope;
+            v[e] = dv * g;
+          } else {
+            sw[e] = fma2(rdout[e] * g, n, sw[e]);
+            a[e] = rdout[e] * rg[e] * n * slope;
+            v[e] = dv;
+          }
+        }
+      }
+      if (dx != nullptr) store_runs<TX, VEC, NV>(dx + row * (M == kResidual ? d.D : d.dgate) + c0, at, on, a);
+      if (dwide_out != nullptr) store_runs<TR, VEC, NV>(dwide_out + ro, at, on, v);
     }
     fetch(turn + stages, stage);
     stage = stage + 1 == stages ? 0 : stage + 1;
-    unit_sum(sums, tpr, sh);
-    const float rstd = rsqrtf(sums[0] / (float)W + eps), mean = sums[1] * rstd / (float)W;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (k * tpr + lane) * VEC;
-      if (!live || c >= W) continue;
-      float a[VEC], b[VEC];
-      if (M == kResidual && scale != nullptr) load_run<VEC>(scale + c, a);
-      if (M == kNormFirst) load_run<VEC>(w + c0 + c, a);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float n = v[k][e] * rstd;
-        float dv = rstd * (uw[k][e] - n * mean);
-        sw[k][e] = fmaf(un[k][e], n, sw[k][e]);
-        if (M == kResidual) {
-          if (want_d) dv += more[k][e];
-          if (ps != nullptr) ss[k][e] = fmaf(dv, other[k][e], ss[k][e]);
-          a[e] = scale != nullptr ? dv * a[e] : dv;
-          b[e] = dv;
-        } else {
-          const float z = other[k][e], sg = sigmoid(z), slope = sg * (1.f + z * (1.f - sg));
-          a[e] = M == kGateFirst ? dv * more[k][e] * slope : more[k][e] * n * a[e] * slope;
-          b[e] = M == kGateFirst ? dv * z * sg : dv;
-        }
-      }
-      if (dx != nullptr) store_run<VEC>(dx + row * (M == kResidual ? d.D : d.dgate) + c0 + c, a);
-      if (dwide_out != nullptr) store_run<VEC>(dwide_out + o + c, b);
-    }
   }
   // the CTA's sums: over its units in order, through shared memory where there are several
   if (VEC > 1) wait_async(0);
-  float *all = reinterpret_cast<float *>(raw);
-  auto put = [&](float (&v)[NV][VEC], float *to) {
+  f2 *all = reinterpret_cast<f2 *>(raw);
+  auto put = [&](f2 (&v)[E], float *to) {
     if (subs > 1) {
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) all[(k * VEC + e) * blockDim.x + threadIdx.x] = v[k][e];
+      for (int e = 0; e < E; ++e) all[e * blockDim.x + threadIdx.x] = v[e];
       __syncthreads();
       if (sub > 0) return;
       for (int u = 1; u < subs; ++u)
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[k][e] += all[(k * VEC + e) * blockDim.x + u * tpr + lane];
+        for (int e = 0; e < E; ++e) v[e] = v[e] + all[e * blockDim.x + u * tpr + lane];
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (k * tpr + lane) * VEC;
-      if (c < W) store_run<VEC>(to + (int64_t)part * d.D + c0 + c, v[k]);
-    }
+    store_runs<float, VEC, NV>(to + (int64_t)part * d.D + c0, at, in, v);
   };
   if (pw != nullptr) put(sw, pw);
   if constexpr (M == kResidual)
     if (ps != nullptr) put(ss, ps);
 }
 
-// The partial sums of one or two vectors: 16 threads a column add every 16th, then one adds those, in order.
-__global__ void __launch_bounds__(512) k_norm_sum(const float *__restrict__ pw, const float *__restrict__ ps, float *dw,
-                                                  float *ds, int64_t D, int n) {
-  __shared__ float sh[16][33];
-  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+// The partial sums of one or two vectors: 32 threads a column add every 32nd, then one adds those, in order.
+__global__ void __launch_bounds__(1024) k_norm_sum(const float *__restrict__ pw, const float *__restrict__ ps,
+                                                   float *dw, float *ds, int64_t D, int n) {
+  __shared__ float sh[32][33];
+  const int column = threadIdx.x % 32, k = threadIdx.x / 32;
+  const int64_t c = (int64_t)blockIdx.x * 32 + column;
   const float *p = blockIdx.y == 0 ? pw : ps;
   float *o = blockIdx.y == 0 ? dw : ds;
   if (o == nullptr) return;
   float s = 0.f;
   if (c < D)
-#pragma unroll 4
-    for (int k = threadIdx.x / 32; k < n; k += 16) s += p[k * D + c];
-  sh[threadIdx.x / 32][threadIdx.x % 32] = s;
+#pragma unroll 8
+    for (int j = k; j < n; j += 32) s += p[j * D + c];
+  sh[k][column] = s;
   __syncthreads();
-  if (threadIdx.x < 32 && c < D) {
+  if (k == 0 && c < D) {
     s = 0.f;
-    for (int k = 0; k < 16; ++k) s += sh[k][threadIdx.x];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s += sh[j][column];
     o[c] = s;
   }
 }
@@ -461,23 +543,24 @@ int parts_of(const NormDims &d) { return (int)std::min<int64_t>(d.rows, kParts);
 
 bool wide_ptr(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Threads a unit of n runs and runs a thread (1, 2 or 4); nv = 0: too many for registers.  Up to 32 runs, a
-// power of two of lanes with one each; else whole warps, with the fewest idle lanes, and as many runs a thread
-// as that allows.
+// Threads a unit of n runs and runs a thread (least .. most, powers of two); nv = 0: too many for registers.  Up
+// to 32 least runs, a power of two of lanes; else whole warps, with the fewest idle lanes, and as many runs a
+// thread as that allows.  limit(nv): the most threads of a CTA.
 struct Split {
   int tpr, nv;
 };
-Split split_unit(int64_t n, int most) {
-  if (n <= 32) {
+template <typename F>
+Split split_unit(int64_t n, int least, int most, F limit) {
+  if (n <= 32 * least) {
     int t = 1;
-    while (t < n) t *= 2;
-    return {t, 1};
+    while (t * least < n) t *= 2;
+    return {t, least};
   }
   Split best = {0, 0};
   int64_t idle = INT64_MAX;
-  for (int nv = most; nv > 0; nv /= 2) {
+  for (int nv = most; nv >= least; nv /= 2) {
     const int64_t t = ((n + nv - 1) / nv + 31) / 32 * 32;
-    if (t <= 1024 && t * nv - n < idle) best = {(int)t, nv}, idle = t * nv - n;
+    if (t <= limit(nv) && t * nv - n < idle) best = {(int)t, nv}, idle = t * nv - n;
   }
   return best;
 }
@@ -486,14 +569,15 @@ template <Mode M, typename TX, typename TR, int VEC>
 bool norm_rows(const TX *x, const float *scale, const TR *wide, const float *w, float eps, TR *wide_out, TX *out,
                const NormDims &d, cudaStream_t st) {
   const int64_t W = d.D / d.G;
-  const Split p = split_unit((W + VEC - 1) / VEC, M == kNormFirst ? 2 : 4);
+  constexpr int least = VEC == 1 ? 2 : 1;
+  const Split p = split_unit((W + VEC - 1) / VEC, least, 4 * least, [](int nv) { return row_threads(nv * VEC); });
   if (p.nv == 0) return false;
   const int threads = p.tpr <= 32 ? 128 : p.tpr, units = threads / p.tpr;
   const unsigned grid = (unsigned)((d.rows * d.G + units - 1) / units);
   auto run = [&](auto *f) { f<<<grid, threads, 0, st>>>(x, scale, wide, w, eps, wide_out, out, d, p.tpr, (int)W); };
-  if (p.nv == 4) run(k_norm_rows<M, TX, TR, VEC, 4>);
-  else if (p.nv == 2) run(k_norm_rows<M, TX, TR, VEC, 2>);
-  else run(k_norm_rows<M, TX, TR, VEC, 1>);
+  if (p.nv == 4 * least) run(k_norm_rows<M, TX, TR, VEC, 4 * least>);
+  else if (p.nv == 2 * least) run(k_norm_rows<M, TX, TR, VEC, 2 * least>);
+  else run(k_norm_rows<M, TX, TR, VEC, least>);
   return true;
 }
 
@@ -515,15 +599,17 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
                         const TR *dwide, TX *dx, TR *dwide_out, float *pw, float *ps, const NormDims &d, int &parts,
                         cudaError_t &err, cudaStream_t st) {
   const int64_t W = d.D / d.G, n = (W + VEC - 1) / VEC;
-  constexpr int most = VEC * NV == 8 ? 640 : 512;
-  const int64_t t = n <= 32 ? split_unit(n, 1).tpr : ((n + NV - 1) / NV + 31) / 32 * 32;
-  if (t > most) return false;
-  const int tpr = (int)t, subs = std::max(1, 256 / tpr), threads = subs * tpr;
-  const int resident = std::max(1, most / threads);
+  constexpr int most = 640;
+  const int tpr = split_unit(n, NV, NV, [](int) { return most; }).tpr;
+  if (tpr == 0) return false;
+  const int subs = std::max(1, 256 / tpr), threads = subs * tpr;
+  const int resident = std::max(1, RES / threads);
   parts = (int)std::max<int64_t>(1, std::min<int64_t>({(d.rows + subs - 1) / subs, 148 * resident / d.G, parts}));
-  const int stage = VEC > 1 ? threads * NV * Pieces<M, TX, TR, VEC>::all * 16 : 0;
-  const int stages = VEC > 1 ? std::max(1, std::min(4, kRingBytes / resident / stage)) : 1;
-  const size_t smem = std::max((size_t)stages * stage, (size_t)threads * VEC * NV * 4);
+  using P = Pieces<M, TX, TR, VEC>;
+  const int stage = VEC > 1 ? threads * NV * P::all * 16 : 0;
+  const int fixed = VEC > 1 ? threads * NV * P::kF * 16 * (M == kResidual && scale != nullptr ? 2 : 1) : 0;
+  const int stages = VEC > 1 ? std::max(1, std::min(4, (kRingBytes / resident - fixed) / stage)) : 1;
+  const size_t smem = std::max((size_t)stages * stage + fixed, (size_t)threads * VEC * NV * 4);
   auto *f = k_norm_backward_rows<M, TX, TR, VEC, NV>;
   err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return true;
@@ -550,8 +636,7 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
   };
   bool done;
   if (vec)
-    done = rows(std::integral_constant<int, 8 / VEC>{}, std::integral_constant<int, VEC>{}) ||
-           rows(std::integral_constant<int, 16 / VEC>{}, std::integral_constant<int, VEC>{});
+    done = rows(std::integral_constant<int, EPT / VEC>{}, std::integral_constant<int, VEC>{});
   else
     done = rows(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
   if (!done) {
@@ -559,7 +644,7 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || (dw == nullptr && ds == nullptr)) return e;
-  k_norm_sum<<<dim3((unsigned)((d.D + 31) / 32), ds != nullptr ? 2 : 1), 512, 0, st>>>(pw, ps, dw, ds, d.D, parts);
+  k_norm_sum<<<dim3((unsigned)((d.D + 31) / 32), ds != nullptr ? 2 : 1), 1024, 0, st>>>(pw, ps, dw, ds, d.D, parts);
   return cudaGetLastError();
 }
 
