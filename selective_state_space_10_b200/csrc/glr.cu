@@ -4,11 +4,14 @@
 //
 // over whole sequences, for one token, and its gradients.
 #include <algorithm>
+#include <atomic>
 #include <stdlib.h>
+#include <stdio.h>
 
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace ssd {
 
@@ -25,7 +28,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-constexpr float kTiny = 1e-37f;  // keeps a root's argument positive where 1 - a^2 is 0
+constexpr float kTiny = 1.2e-38f;  // keeps a root's argument positive where 1 - a^2 is 0
 
 // exp(-v), with overflow to infinity; exp_neg_finite stops at 2^126, so that e / (1 + e) stays 1
 __device__ __forceinline__ f2 exp_neg(f2 v) { return ex2(v * both(-kLog2e)); }
@@ -39,6 +42,7 @@ __device__ __forceinline__ f2 exp_neg_finite(f2 v) {
 // step of fp32), a = 2^n (1 + p), v = (1 - 2^n) - 2^n p.  1 - a^2 = v (1 + a) then loses nothing for decays close
 // to 1; an exp(L) rounded near 1 and subtracted would, and its error would be carried through every step of a
 // long memory.  The exponential unit, which the gates already fill, is not used.
+template <bool kSmall>  // kSmall: a small a is wanted to full relative precision too, not only to that of 1
 __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
   const float2 s = split(L);
   L = mk(max_nan(s.x, -87.f), max_nan(s.y, -87.f));  // n >= -126
@@ -54,18 +58,18 @@ __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
   const float2 i = split(t);
   const f2 two_n = mk(__int_as_float((__float_as_int(i.x) << 23) + 0x3f800000),
                       __int_as_float((__float_as_int(i.y) << 23) + 0x3f800000));
-  a = two_n * fma2(p, both(-1.f), both(1.f));
   v = fma2(two_n, p, fma2(two_n, both(-1.f), both(1.f)));
+  a = kSmall ? two_n * fma2(p, both(-1.f), both(1.f)) : fma2(v, both(-1.f), both(1.f));
 }
 
 // One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x, as x rest / sqrt(rest (1 + e)^2) with
 // rest = 1 - a^2 and e = exp(-i): one root in place of a root and a reciprocal.  A shut input gate (e and its
-// square overflow) gives 0.
+// square overflow) gives 0; where a is exactly 1, rest is kTiny and 1e-19 of x comes in.
 __device__ __forceinline__ void gate(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b) {
   f2 v;
-  decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
-  const f2 rest = v * (a + both(1.f)), o = exp_neg(i) + both(1.f);
-  b = x * rest * rsqrt_approx(o * o * (rest + both(kTiny)));
+  decay<false>(A * rcp(exp_neg(r) + both(1.f)), a, v);
+  const f2 rest = fma2(v, a, v + both(kTiny)), o = exp_neg(i) + both(1.f);
+  b = x * rest * rsqrt_approx(o * o * rest);
 }
 
 // One step back: c (in: c_{t+1}, out: c_t = a_t g_t), the gradients of x, r and i, and dA's term.
@@ -124,16 +128,19 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
 // state and runs its 8 steps: every array is read and written once.  Where the channels alone
 // leave the GPU idle, a cluster of up to 8 CTAs shares a sequence, a tile each in turn: the
 // CTAs' own A h + H go to the ranks behind them through distributed shared memory.
-#ifndef PW
-#define PW 8
-#define PT 8
-#define PB 2
-#define BW 8
-#define BT 4
-#define BB 3
+#ifndef PT
+#define PT 16
+#define PW 4
+#define BW 4
+#define PB 3
+#define BT 8
+#define BB 4
 #endif
+// warps, tokens a warp and CTAs an SM of each scan
+template <typename T> struct PrefillShape { static constexpr int W = sizeof(T) == 2 ? PW : 4, N = sizeof(T) == 2 ? PT : 8, kResident = sizeof(T) == 2 ? PB : 3; };
+template <typename T> struct BackwardShape { static constexpr int W = sizeof(T) == 2 ? BW : 4, N = sizeof(T) == 2 ? BT : 4, kResident = sizeof(T) == 2 ? BB : 4; };
 constexpr int kCh = 64;  // channels a CTA
-constexpr int kMaxRanks = 8;
+constexpr int kMaxRanks = 16;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -238,7 +245,7 @@ template <int kW>
 struct Links {
   Link carry[2][32];  // H: the state entering the tile
   Link warp[2][kW][32];
-  Link rank[2][kMaxRanks][32];
+  // behind it, in a cluster: Link rank[2][ranks][32]
 };
 __device__ __forceinline__ Link load_link(const Link &l) {
   const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&l);
@@ -252,6 +259,9 @@ struct Exchange {
   Links<kW> &l;
   int warp, lane, rank, ranks;
   Link before;  // the warps before this one
+  __device__ __forceinline__ Link *from_rank(int par, int k) const {
+    return reinterpret_cast<Link *>(&l + 1) + (par * ranks + k) * 32 + lane;
+  }
   __device__ __forceinline__ void prefix(int par) {
     before = {both(1.f), both(0.f)};
     for (int w = 0; w < warp; ++w) before = then(before, load_link(l.warp[par][w][lane]));
@@ -263,7 +273,7 @@ struct Exchange {
       prefix(par);
       if (warp == kW - 1) {
         const Link all = then(before, mine);
-        for (int k = rank + 1; k < ranks; ++k) store_rank(&l.rank[par][rank][lane], k, all);
+        for (int k = rank + 1; k < ranks; ++k) store_rank(from_rank(par, rank), k, all);
       }
       arrive_ranks(warp == kW - 1);
     }
@@ -278,7 +288,7 @@ struct Exchange {
     f2 h = l.carry[par][lane].H;
     if constexpr (kCluster)
       for (int k = 0; k < rank; ++k) {
-        const Link f = load_link(l.rank[par][k][lane]);
+        const Link f = load_link(*from_rank(par, k));
         h = fma2(f.A, h, f.H);
       }
     return fma2(before.A, h, before.H);
@@ -298,11 +308,11 @@ struct Exchange {
 template <typename T, int N, int kW, int kT>
 struct ScanSmem {
   T in[kW][2][N][kT][kCh];
-  Links<kW> links;  // the last member: without a cluster its `rank` is not allocated
+  Links<kW> links;  // the last member: the ranks' updates follow
 };
 template <typename T, int N, int kW, int kT>
 size_t scan_smem(int ranks) {
-  return sizeof(ScanSmem<T, N, kW, kT>) - (ranks > 1 ? 0 : sizeof(Links<kW>::rank));
+  return sizeof(ScanSmem<T, N, kW, kT>) + (ranks > 1 ? 2 * ranks * 32 * sizeof(Link) : 0);
 }
 
 // A CTA's place in the grid.
@@ -328,7 +338,7 @@ __device__ __forceinline__ Place place(int64_t D, int blocks) {
 }
 
 template <typename T, int CW, bool kCluster, int kW, int kT>
-__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? PB : (PB + 1) / 2)
+__global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
     k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                   const float *__restrict__ A, const float *init, T *__restrict__ h, float *final_state, GlrDims d,
                   int blocks) {
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
 // and the rest is formed when g is known.  A tile is 5 inputs deep, which leaves two CTAs an SM for bf16
 // and one for fp32.
 template <typename T, int CW, bool kCluster, int kW, int kT>
-__global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? BB : (BB + 1) / 2)
+__global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     k_glr_backward(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                    const float *__restrict__ A, const float *__restrict__ init, const T *__restrict__ h,
                    const T *__restrict__ dh, const float *dfinal, T *__restrict__ dx, T *__restrict__ dr,
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? BB : (BB + 1) / 2)
     f2 a[kT], v[kT];
 #pragma unroll
     for (int j = kT - 1; j >= 0; --j)
-      decay(Ac * rcp(exp_neg(load2(&in[0][j][2 * p.lane])) + both(1.f)), a[j], v[j]);
+      decay<true>(Ac * rcp(exp_neg(load2(&in[0][j][2 * p.lane])) + both(1.f)), a[j], v[j]);
     if (t < 0) {  // tokens before the first leave c as it is
 #pragma unroll
       for (int j = 0; j < kT; ++j)
@@ -528,38 +538,65 @@ __global__ void __launch_bounds__(kW * 32, sizeof(T) == 2 ? BB : (BB + 1) / 2)
 __global__ void __launch_bounds__(128) k_glr_sum(const float *__restrict__ part, float *__restrict__ dA, int64_t D,
                                                  int64_t n) {
   const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  sm100::grid_dep_wait();  // launched before the partial sums are complete
   if (c >= D) return;
   float s = 0.f;
+#pragma unroll 8
   for (int64_t k = 0; k < n; ++k) s += part[k * D + c];
   dA[c] = s;
 }
 
 bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// CTAs that share a sequence: as many as the GPU holds at once (`resident` an SM) and the
-// sequence has tiles for.
-int pick_ranks(int64_t ctas, int64_t L, int tile, int resident) {
-  if (const char *e = getenv("RANKS")) return std::max(1, std::min(atoi(e), (int)((L + tile - 1) / tile)));
-  const int64_t room = (int64_t)148 * resident / ctas, tiles = (L + tile - 1) / tile;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({room, tiles, kMaxRanks}));
-}
-
-template <typename... P, typename... V>
-cudaError_t launch_ranks(void (*f)(P...), int64_t ctas, int ranks, int warps, size_t smem, cudaStream_t st,
-                         V... v) {
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
+// The launch of a scan kernel: `ranks` CTAs share a sequence and are a cluster.
+template <typename F>
+cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, F *f, int64_t ctas, int ranks, int warps, size_t smem,
+                   cudaStream_t st) {
+  cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3((unsigned)(ctas * ranks));
   cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim = {(unsigned)ranks, 1, 1};
   cfg.attrs = &at;
   cfg.numAttrs = ranks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, f, v...);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
+// How many CTAs share a sequence: the most, up to kMaxRanks and one a tile, whose clusters the GPU holds all at once.
+// What it holds depends on how clusters of a size fill its graphics clusters (2.7B-shaped prefill, 80 blocks of
+// channels: 5 ranks 52 us, 4 60 us; 6 need a second wave, 67 us), so each kernel asks the runtime once.
+template <typename T, int N, int kW, int kT, typename... P>
+cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) {
+  static std::atomic<int> held[kMaxRanks + 1];  // clusters of each size that fit, + 1; 0: not asked yet
+  ranks = (int)std::min<int64_t>((L + kW * kT - 1) / (kW * kT), kMaxRanks);
+  if (const char *e = getenv("RANKS")) { ranks = std::min(ranks, atoi(e)); return cudaSuccess; }
+  for (; ranks > 1; --ranks) {
+    int fit = held[ranks].load(std::memory_order_relaxed) - 1;
+    if (fit < 0) {
+      cudaLaunchConfig_t cfg;
+      cudaLaunchAttribute at;
+      cudaError_t e = set_up(cfg, at, many, 1, ranks, kW, scan_smem<T, N, kW, kT>(ranks), nullptr);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, many, &cfg);
+      if (e != cudaSuccess) return e;
+      held[ranks].store(fit + 1, std::memory_order_relaxed);
+      if (getenv("GLRDBG")) printf("ranks %d fit %d\n", ranks, fit), fflush(stdout);
+    }
+    if (ctas <= fit) break;
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int N, int kW, int kT, typename... P, typename... V>
+cudaError_t launch_scan(void (*one)(P...), void (*many)(P...), int64_t ctas, int ranks, cudaStream_t st, V... v) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute at;
+  auto *f = ranks > 1 ? many : one;
+  cudaError_t e = set_up(cfg, at, f, ctas, ranks, kW, scan_smem<T, N, kW, kT>(ranks), st);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, f, v...);
 }
 
 }  // namespace
@@ -570,11 +607,13 @@ cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *
   const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
   constexpr int E = 16 / sizeof(T);
   const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && d.D % E == 0 && d.row % E == 0;
-  constexpr int W = PW, N = PT;
-  const int ranks = pick_ranks(ctas, d.L, W * N, sizeof(T) == 2 ? PB : (PB + 1) / 2);
+  using Shape = PrefillShape<T>;
+  constexpr int W = Shape::W, N = Shape::N;
   auto run = [&](auto *one, auto *many) {
-    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, W, scan_smem<T, 3, W, N>(ranks), st, x, r, i, A, init, h,
-                        final_state, d, (int)blocks);
+    int ranks;
+    cudaError_t e = pick_ranks<T, 3, W, N>(many, ctas, d.L, ranks);
+    if (e != cudaSuccess) return e;
+    return launch_scan<T, 3, W, N>(one, many, ctas, ranks, st, x, r, i, A, init, h, final_state, d, (int)blocks);
   };
   if (w16) return run(k_glr_prefill<T, 16, false, W, N>, k_glr_prefill<T, 16, true, W, N>);
   constexpr int CW = sizeof(T) == 4 ? 4 : 0;
@@ -599,18 +638,29 @@ cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float 
   constexpr int E = 16 / sizeof(T);
   const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && wide(dh) && wide(dx) && wide(dr) && wide(di) &&
                    d.D % E == 0 && d.row % E == 0 && d.grad % E == 0;
-  constexpr int W = BW, N = BT;
-  const int ranks = pick_ranks(ctas, d.L, W * N, sizeof(T) == 2 ? BB : (BB + 1) / 2);
+  using Shape = BackwardShape<T>;
+  constexpr int W = Shape::W, N = Shape::N;
+  int ranks = 1;
   auto run = [&](auto *one, auto *many) {
-    return launch_ranks(ranks > 1 ? many : one, ctas, ranks, W, scan_smem<T, 5, W, N>(ranks), st, x, r, i, A, init, h, dh,
-                        dfinal, dx, dr, di, dinit, part, d, (int)blocks);
+    cudaError_t e = pick_ranks<T, 5, W, N>(many, ctas, d.L, ranks);
+    if (e != cudaSuccess) return e;
+    return launch_scan<T, 5, W, N>(one, many, ctas, ranks, st, x, r, i, A, init, h, dh, dfinal, dx, dr, di, dinit, part, d,
+                                   (int)blocks);
   };
   constexpr int CW = sizeof(T) == 4 ? 4 : 0;
   cudaError_t e = w16 ? run(k_glr_backward<T, 16, false, W, N>, k_glr_backward<T, 16, true, W, N>)
                       : run(k_glr_backward<T, CW, false, W, N>, k_glr_backward<T, CW, true, W, N>);
   if (e != cudaSuccess) return e;
-  k_glr_sum<<<(unsigned)((d.D + 127) / 128), 128, 0, st>>>(part, dA, d.D, d.b * ranks);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((d.D + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_glr_sum, (const float *)part, dA, d.D, d.b * ranks);
 }
 
 #define SSD_GLR_INSTANCES(T)                                                                                           \

@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace ssd {
 
@@ -148,23 +149,26 @@ __device__ __forceinline__ float total(f2 v) {
   return s.x + s.y;
 }
 
-// A sum (or a pair of them) over a unit's threads, in every one of them.  Units of several warps meet at a barrier of
-// their own; sh: one a warp of the CTA, not used by the call before (two buffers in turn).
 __device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
 __device__ __forceinline__ f2 from_lane(f2 v, int o) { return {__shfl_xor_sync(0xffffffffu, v.v, o)}; }
-template <typename S>
+// A sum (or a pair of them) over a unit's threads, in every one of them; sh: one a warp of the CTA, not used by the
+// call before (two buffers in turn).  kSeveral: units of several warps in one CTA, which meet at barriers of their own
+// (a kernel with numbered barriers takes all 16 of a CTA, and an SM has 64: no more than 4 CTAs fit).
+template <bool kSeveral, typename S>
 __device__ __forceinline__ S unit_sum(S v, int tpr, S *sh) {
   for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) v = v + from_lane(v, o);
   if (tpr <= 32) return v;
-  const int warp = threadIdx.x >> 5, warps = tpr >> 5, unit = threadIdx.x / tpr;
-  if ((threadIdx.x & 31) == 0) sh[warp] = v;
-  if (tpr == blockDim.x)
-    __syncthreads();
-  else
+  const int warps = tpr >> 5;
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  if constexpr (kSeveral) {
+    const int unit = threadIdx.x / tpr;
     asm volatile("bar.sync %0, %1;" ::"r"(unit + 1), "r"(tpr) : "memory");
-  v = sh[unit * warps];
-#pragma unroll 4
-  for (int j = 1; j < warps; ++j) v = v + sh[unit * warps + j];
+    sh += unit * warps;
+  } else {
+    __syncthreads();
+  }
+  v = sh[0];
+  for (int j = 1; j < warps; ++j) v = v + sh[j];
   return v;
 }
 
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(row_threads(NV *VEC))
   f2 ss = both(0.f);
 #pragma unroll
   for (int e = 0; e < E; ++e) ss = fma2(v[e], v[e], ss);
-  const f2 rstd = both(rsqrtf(unit_sum(total(ss), tpr, sh) / (float)W + eps));
+  const f2 rstd = both(rsqrtf(unit_sum<false>(total(ss), tpr, sh) / (float)W + eps));
   if (M == kResidual && wide_out != nullptr) store_runs<TR, VEC, NV>(wide_out + row * d.D + c0, at, on, v);
   Runs<float, VEC, NV> rg;
   rg.load(w + c0, at);
@@ -310,13 +314,8 @@ __device__ __forceinline__ void wait_async(int left) {  // at most `left` (0 .. 
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-#ifndef EPT
-#define EPT 8
-#define T8 640
-#define RES 640
-#define RB 216
-#endif
-constexpr int kRingBytes = RB * 1024;  // of an SM's shared memory, all its CTAs together
+constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory, all its CTAs together
+constexpr int kRowThreads = 640;        // of an SM, all its CTAs together: 96 registers each
 
 // 16-byte pieces of a run of VEC channels of the four inputs, and of an fp32 vector
 template <Mode M, typename TX, typename TR, int VEC>
@@ -329,7 +328,7 @@ struct Pieces {
 };
 
 template <Mode M, typename TX, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(640)
+__global__ void __launch_bounds__(kRowThreads)
     k_norm_backward_rows(const TX *__restrict__ x, const float *__restrict__ scale, const TR *__restrict__ wide,
                          const float *__restrict__ w, float eps, const TX *__restrict__ dout, const TR *dwide, TX *dx,
                          TR *dwide_out, float *__restrict__ pw, float *__restrict__ ps, NormDims d, int tpr, int W,
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(640)
       s0 = fma2(v[e], v[e], s0);
       s1 = fma2(uw[e], v[e], s1);
     }
-    const float2 sums = split(unit_sum(mk(total(s0), total(s1)), tpr, sh[turn & 1]));
+    const float2 sums = split(unit_sum<true>(mk(total(s0), total(s1)), tpr, sh[turn & 1]));
     if (live) {  // nothing was fetched for a row past the last one
       const float rs1 = rsqrtf(sums.x / (float)W + eps);
       const f2 rstd = both(rs1), mean = both(-sums.y * rs1 / (float)W);
@@ -524,6 +523,7 @@ __global__ void __launch_bounds__(1024) k_norm_sum(const float *__restrict__ pw,
   const int64_t c = (int64_t)blockIdx.x * 32 + column;
   const float *p = blockIdx.y == 0 ? pw : ps;
   float *o = blockIdx.y == 0 ? dw : ds;
+  sm100::grid_dep_wait();  // launched before the partial sums are complete
   if (o == nullptr) return;
   float s = 0.f;
   if (c < D)
@@ -599,11 +599,10 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
                         const TR *dwide, TX *dx, TR *dwide_out, float *pw, float *ps, const NormDims &d, int &parts,
                         cudaError_t &err, cudaStream_t st) {
   const int64_t W = d.D / d.G, n = (W + VEC - 1) / VEC;
-  constexpr int most = 640;
-  const int tpr = split_unit(n, NV, NV, [](int) { return most; }).tpr;
+  const int tpr = split_unit(n, NV, NV, [](int) { return kRowThreads; }).tpr;
   if (tpr == 0) return false;
   const int subs = std::max(1, 256 / tpr), threads = subs * tpr;
-  const int resident = std::max(1, RES / threads);
+  const int resident = std::max(1, kRowThreads / threads);
   parts = (int)std::max<int64_t>(1, std::min<int64_t>({(d.rows + subs - 1) / subs, 148 * resident / d.G, parts}));
   using P = Pieces<M, TX, TR, VEC>;
   const int stage = VEC > 1 ? threads * NV * P::all * 16 : 0;
@@ -611,7 +610,7 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
   const int stages = VEC > 1 ? std::max(1, std::min(4, (kRingBytes / resident - fixed) / stage)) : 1;
   const size_t smem = std::max((size_t)stages * stage + fixed, (size_t)threads * VEC * NV * 4);
   auto *f = k_norm_backward_rows<M, TX, TR, VEC, NV>;
-  err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 48 * 1024) err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return true;
   f<<<(unsigned)(parts * d.G), threads, smem, st>>>(x, scale, wide, w, eps, dout, dwide, dx, dwide_out, pw, ps, d, tpr,
                                                     (int)W, parts, stages);
@@ -634,9 +633,20 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
     return norm_backward_rows<M, TX, TR, decltype(v)::value, decltype(nv)::value>(
         x, scale, wide, w, eps, dout, dwide, dx, dwide_out, pw, ps, d, parts, e, st);
   };
+  // 8 or 16 channels a thread.  The residual norm's two vectors of sums fill the registers at 8 (65536 x 768, bf16
+  // with an fp32 stream: 200 us, at 16 330); the gated norm's one leaves room for 16, and half the reductions a row
+  // (4096 x 5120: 78 us, at 8 92), unless more lanes are left idle than at 8 (43690 x 768: 136 us, at 8 111).  Rows
+  // too long for 8 take 16 in any case.
+  const int64_t W = d.D / d.G;
+  auto idle = [&](int n) {
+    const Split p = split_unit((W + VEC - 1) / VEC, n / VEC, n / VEC, [](int) { return kRowThreads; });
+    return p.tpr == 0 ? INT64_MAX : p.tpr * n - W;
+  };
+  const bool more = M == kResidual ? idle(8) == INT64_MAX : idle(16) <= idle(8);
   bool done;
   if (vec)
-    done = rows(std::integral_constant<int, EPT / VEC>{}, std::integral_constant<int, VEC>{});
+    done = more ? rows(std::integral_constant<int, 16 / VEC>{}, std::integral_constant<int, VEC>{})
+                : rows(std::integral_constant<int, 8 / VEC>{}, std::integral_constant<int, VEC>{});
   else
     done = rows(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
   if (!done) {
@@ -644,8 +654,16 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || (dw == nullptr && ds == nullptr)) return e;
-  k_norm_sum<<<dim3((unsigned)((d.D + 31) / 32), ds != nullptr ? 2 : 1), 1024, 0, st>>>(pw, ps, dw, ds, d.D, parts);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((d.D + 31) / 32), ds != nullptr ? 2 : 1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_sum, (const float *)pw, (const float *)ps, dw, ds, d.D, parts);
 }
 
 }  // namespace
