@@ -5,8 +5,6 @@
 // over whole sequences, for one token, and its gradients.
 #include <algorithm>
 #include <atomic>
-#include <stdlib.h>
-#include <stdio.h>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -121,24 +119,25 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
 }
 
 // The scans.  A CTA takes 64 channels (two a lane) of one batch row and walks the sequence in
-// tiles of 64 tokens, 8 a warp.  Each warp copies its own tokens of the next tiles into
-// shared memory (two stages) while it forms the gates of this one, keeps its 8 decays and
-// input terms in registers, and publishes what they do to a state, h -> A h + H, as one
-// 16-byte word a lane.  After a barrier a warp applies the warps before it to the carried
-// state and runs its 8 steps: every array is read and written once.  Where the channels alone
-// leave the GPU idle, a cluster of up to 8 CTAs shares a sequence, a tile each in turn: the
-// CTAs' own A h + H go to the ranks behind them through distributed shared memory.
-#ifndef PT
-#define PT 16
-#define PW 4
-#define BW 4
-#define PB 3
-#define BT 8
-#define BB 4
-#endif
-// warps, tokens a warp and CTAs an SM of each scan
-template <typename T> struct PrefillShape { static constexpr int W = sizeof(T) == 2 ? PW : 4, N = sizeof(T) == 2 ? PT : 8, kResident = sizeof(T) == 2 ? PB : 3; };
-template <typename T> struct BackwardShape { static constexpr int W = sizeof(T) == 2 ? BW : 4, N = sizeof(T) == 2 ? BT : 4, kResident = sizeof(T) == 2 ? BB : 4; };
+// tiles, kT tokens a warp.  Each warp copies its own tokens of the next tiles into shared memory
+// (two stages) while it forms the gates of this one, keeps its decays and input terms in
+// registers, and publishes what they do to a state, h -> A h + H, as one 16-byte word a lane.
+// After a barrier a warp applies the warps before it to the carried state and runs its steps:
+// every array is read and written once.  Where the channels alone leave the GPU idle, a cluster
+// of CTAs shares a sequence, a tile each in turn: the CTAs' own A h + H go to the ranks behind
+// them through distributed shared memory.
+// Warps, tokens a warp and CTAs an SM of each scan.  Long runs of tokens amortise a tile's exchange, small CTAs keep the
+// SMs evenly loaded (2.7B-shaped bf16 prefill: 4 x 16 47.8 us, 4 x 12 54.0, 4 x 8 54.3, 2 x 16 57.2, 8 x 16 66.5 us;
+// long-context bf16 gradient: 4 x 12 381 us, 4 x 8 408, 2 x 12 437, 4 x 4 490, 8 x 8 509 us).  fp32 tiles are twice
+// the bytes and bound by them: any of these shapes runs the same there.
+template <typename T>
+struct PrefillShape {
+  static constexpr int W = 4, N = sizeof(T) == 2 ? 16 : 8, kResident = 3;
+};
+template <typename T>
+struct BackwardShape {
+  static constexpr int W = 4, N = sizeof(T) == 2 ? 12 : 4, kResident = sizeof(T) == 2 ? 3 : 4;
+};
 constexpr int kCh = 64;  // channels a CTA
 constexpr int kMaxRanks = 16;
 
@@ -217,15 +216,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-// The cluster's barrier.  What a warp has written to distributed shared memory before a releasing arrival is seen
-// after the wait; warps that wrote nothing there arrive relaxed, and do not wait for their stores to drain.
-__device__ __forceinline__ void arrive_ranks(bool release) {
-  if (release)
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  else
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+// The cluster's barrier; what was written to (distributed) shared memory before it is seen after.
+__device__ __forceinline__ void sync_ranks() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void wait_ranks() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // A state update h -> A h + H of a lane's two channels.
 struct alignas(16) Link {
@@ -234,75 +229,128 @@ struct alignas(16) Link {
 __device__ __forceinline__ Link then(Link first, Link second) {
   return {first.A * second.A, fma2(second.A, first.H, second.H)};
 }
-__device__ __forceinline__ void store_rank(Link *p, uint32_t rank, Link v) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(a), "l"(v.A.v), "l"(v.H.v) : "memory");
-}
+constexpr int kSlots = 3;  // tiles whose messages a rank may hold
 
-// What the warps and ranks of a scan tell one another, by parity of the tile.
+// What the warps and ranks of a scan tell one another.
 template <int kW>
 struct Links {
-  Link carry[2][32];  // H: the state entering the tile
+  Link carry[kSlots][32];  // H: the state entering the tile
   Link warp[2][kW][32];
-  // behind it, in a cluster: Link rank[2][ranks][32]
+  uint64_t arrived[kSlots];  // mbarriers: a tile's messages from other ranks are here
+  uint64_t pad[kSlots % 2];
+  // behind it, in a cluster: Link rank[kSlots][ranks][32]
 };
 __device__ __forceinline__ Link load_link(const Link &l) {
   const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&l);
   return {{u.x}, {u.y}};
 }
 
-// The exchange of a tile, in two halves so that a warp has other work while it waits: `publish` gives its own
-// update away, `collect` returns the state that enters its tokens.  Every warp of every rank calls each once a tile.
+// The exchange of a tile: `publish` gives a warp's own update away, `collect` returns the state that enters its
+// tokens; every warp of every rank calls each once a tile, then `next`.  Between the ranks of a cluster the updates
+// travel as st.async messages that count themselves in on the receiver's mbarrier, so no rank waits for one behind
+// it, and no warp for its own stores to drain, as both would at a cluster barrier a tile (2.7B-shaped bf16 prefill, 5
+// ranks: 47.8 us against 52.6 us; fp32: 58 against 72 us).
+// Three slots are enough: a rank sends tile k + 3 only after it got the state that enters tile k + 2, which the last
+// rank sent after every rank had published k + 1, and so had collected k.
+// A wait gives up after 2 s of global time; the state is then NaN from there on.
 template <bool kCluster, int kW>
 struct Exchange {
   Links<kW> &l;
   int warp, lane, rank, ranks;
-  Link before;  // the warps before this one
-  __device__ __forceinline__ Link *from_rank(int par, int k) const {
-    return reinterpret_cast<Link *>(&l + 1) + (par * ranks + k) * 32 + lane;
+  int par, slot, phase;  // of the tile
+  bool later, lost;      // not the first tile; a wait has expired
+  Link before;           // the warps before this one
+
+  __device__ __forceinline__ Exchange(Links<kW> &links, int warp, int lane, int rank, int ranks)
+      : l(links), warp(warp), lane(lane), rank(rank), ranks(ranks), par(0), slot(0), phase(0), later(false), lost(false) {}
+  // The state that enters the first tile, and the barriers; then all threads of all ranks may go on.
+  __device__ __forceinline__ void start(f2 h) {
+    if (warp == 0) l.carry[0][lane].H = h;
+    if constexpr (kCluster) {
+      if (threadIdx.x == 0) {
+        for (int k = 0; k < kSlots; ++k) sm100::mbar_init(&l.arrived[k], 1);
+        sm100::mbar_fence_init();
+      }
+      sync_ranks();
+    }
   }
-  __device__ __forceinline__ void prefix(int par) {
+  __device__ __forceinline__ Link *from_rank(int slot, int k) const {
+    return reinterpret_cast<Link *>(&l + 1) + (slot * ranks + k) * 32 + lane;
+  }
+  // One lane's 16 bytes of a message of 512.
+  __device__ __forceinline__ void send(Link *to, int slot, int rank, Link v) const {
+    uint32_t a, b;
+    const float2 A = split(v.A), H = split(v.H);
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(to)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_addr(&l.arrived[slot])), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "f"(A.x), "f"(A.y), "f"(H.x), "f"(H.y), "r"(b)
+                 : "memory");
+  }
+  __device__ __forceinline__ bool wait() const {
+    const uint32_t bar = smem_addr(&l.arrived[slot]);
+    uint64_t t0 = 0;
+    while (true) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(phase), "r"(20000u)
+          : "memory");
+      if (ok) return true;
+      const uint64_t t = sm100::globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > 2000000000ull) return false;
+    }
+  }
+  __device__ __forceinline__ void prefix() {
     before = {both(1.f), both(0.f)};
     for (int w = 0; w < warp; ++w) before = then(before, load_link(l.warp[par][w][lane]));
   }
-  __device__ __forceinline__ void publish(int par, Link mine) {
+  __device__ __forceinline__ void publish(Link mine) {
     l.warp[par][warp][lane] = mine;
-    if constexpr (kCluster) {
-      __syncthreads();
-      prefix(par);
+    __syncthreads();
+    prefix();
+    if constexpr (kCluster)
       if (warp == kW - 1) {
         const Link all = then(before, mine);
-        for (int k = rank + 1; k < ranks; ++k) store_rank(from_rank(par, rank), k, all);
+        for (int k = rank + 1; k < ranks; ++k) send(from_rank(slot, rank), slot, k, all);
+        if (lane == 0) sm100::mbar_arrive_expect_tx(&l.arrived[slot], 512u * (rank + (later ? 1 : 0)));
       }
-      arrive_ranks(warp == kW - 1);
-    }
   }
-  __device__ __forceinline__ f2 collect(int par) {
-    if constexpr (kCluster) {
-      wait_ranks();
-    } else {
-      __syncthreads();
-      prefix(par);
-    }
-    f2 h = l.carry[par][lane].H;
+  __device__ __forceinline__ f2 collect() {
     if constexpr (kCluster)
+      if (!lost) lost = !wait();
+    f2 h = l.carry[slot][lane].H;
+    if constexpr (kCluster) {
       for (int k = 0; k < rank; ++k) {
-        const Link f = load_link(*from_rank(par, k));
+        const Link f = load_link(*from_rank(slot, k));
         h = fma2(f.A, h, f.H);
       }
+      if (lost) h = both(__int_as_float(0x7fffffff));
+    }
     return fma2(before.A, h, before.H);
   }
-  // The state after the tile's last token, from the last warp of the last rank, for the next tile (not
-  // after the last one: a rank may have left by then).
-  __device__ __forceinline__ void leave(int par, f2 h) {
-    const Link v = {both(0.f), h};
-    if constexpr (kCluster)
-      for (int k = 0; k < ranks; ++k) store_rank(&l.carry[par ^ 1][lane], k, v);
-    else
-      l.carry[par ^ 1][lane] = v;
+  // To the next tile, which `h`, the state after this warp's tokens, enters if the warp is the last of the last rank.
+  __device__ __forceinline__ void next(f2 h) {
+    par ^= 1;
+    later = true;
+    if (++slot == kSlots) slot = 0, phase ^= 1;
+    if (last()) {
+      const Link v = {both(0.f), h};
+      if constexpr (kCluster)
+        for (int k = 0; k < ranks; ++k) send(&l.carry[slot][lane], slot, k, v);
+      else
+        l.carry[slot][lane] = v;
+    }
   }
   __device__ __forceinline__ bool last() const { return warp == kW - 1 && rank == ranks - 1; }
+  // No rank leaves while another may still write to it.
+  __device__ __forceinline__ void finish() const {
+    if constexpr (kCluster) sync_ranks();
+  }
 };
 
 template <typename T, int N, int kW, int kT>
@@ -312,7 +360,7 @@ struct ScanSmem {
 };
 template <typename T, int N, int kW, int kT>
 size_t scan_smem(int ranks) {
-  return sizeof(ScanSmem<T, N, kW, kT>) + (ranks > 1 ? 2 * ranks * 32 * sizeof(Link) : 0);
+  return sizeof(ScanSmem<T, N, kW, kT>) + (ranks > 1 ? kSlots * ranks * 32 * sizeof(Link) : 0);
 }
 
 // A CTA's place in the grid.
@@ -346,7 +394,7 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 3, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 3, kW, kT> *>(raw);
   const Place p = place<kCluster>(d.D, blocks);
-  Exchange<kCluster, kW> ex{sm.links, p.warp, p.lane, p.rank, p.ranks, {}};
+  Exchange<kCluster, kW> ex(sm.links, p.warp, p.lane, p.rank, p.ranks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
   const int64_t t0 = p.rank * kTile + p.warp * kT;  // this warp's first token
@@ -383,11 +431,7 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   };
   load(0, left);
   load(1, left - step);
-  if (p.warp == 0) sm.links.carry[0][p.lane].H = init != nullptr ? load_n(init + p.b * d.D + p.c, p.n) : both(0.f);
-  if constexpr (kCluster) {  // no rank writes to another that has not started
-    arrive_ranks(true);
-    wait_ranks();
-  }
+  ex.start(init != nullptr ? load_n(init + p.b * d.D + p.c, p.n) : both(0.f));
   T *out = h + (p.b * d.L + t0) * d.D + p.c;
   f2 s = both(0.f);
   for (int64_t tile = 0; tile < tiles; ++tile, left -= step, out += step * d.D) {
@@ -398,8 +442,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
 #pragma unroll
     for (int j = 1; j < kT; ++j) all = then(all, {a[j], v[j]});
     load(par, left - 2 * step);
-    ex.publish(par, all);
-    s = ex.collect(par);
+    ex.publish(all);
+    s = ex.collect();
     if (left >= kT) {
 #pragma unroll
       for (int j = 0; j < kT; ++j) {
@@ -413,9 +457,10 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
         if (j < left) store2<CW == 16>(out + j * d.D, s, p.n);
       }
     }
-    if (ex.last() && tile + 1 < tiles) ex.leave(par, s);
+    if (tile + 1 < tiles) ex.next(s);
   }
   if (ex.last()) store2<false>(final_state + p.b * d.D + p.c, s, p.n);
+  ex.finish();
 }
 
 template <typename T>
@@ -447,7 +492,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 5, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 5, kW, kT> *>(raw);
   const Place p = place<kCluster>(d.D, blocks);
-  Exchange<kCluster, kW> ex{sm.links, p.warp, p.lane, p.rank, p.ranks, {}};
+  Exchange<kCluster, kW> ex(sm.links, p.warp, p.lane, p.rank, p.ranks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
   // this warp's tokens are t .. t + 7; those below 0 lie before the sequence
@@ -474,11 +519,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   };
   load(0, t);
   load(1, t - step);
-  if (p.warp == 0) sm.links.carry[0][p.lane].H = dfinal != nullptr ? load_n(dfinal + p.b * d.D + p.c, p.n) : both(0.f);
-  if constexpr (kCluster) {  // no rank writes to another that has not started
-    arrive_ranks(true);
-    wait_ranks();
-  }
+  ex.start(dfinal != nullptr ? load_n(dfinal + p.b * d.D + p.c, p.n) : both(0.f));
   int64_t to = (p.b * d.L + t) * d.grad + p.c;
   f2 s = both(0.f), dA = both(0.f);
   for (int64_t tile = 0; tile < tiles; ++tile, t -= step, to -= step * d.grad) {
@@ -501,8 +542,8 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
 #pragma unroll
       for (int j = kT - 1; j >= 0; --j) all = then(all, {a[j], a[j] * load2(&in[1][j][2 * p.lane])});
     }
-    ex.publish(par, all);
-    s = ex.collect(par);
+    ex.publish(all);
+    s = ex.collect();
 #pragma unroll
     for (int j = kT - 1; j >= 0; --j) {
       if (!any) break;
@@ -519,7 +560,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     }
     __syncwarp();
     load(par, t - 2 * step);
-    if (ex.last() && tile + 1 < tiles) ex.leave(par, s);
+    if (tile + 1 < tiles) ex.next(s);
   }
   if (dinit != nullptr && ex.last()) store2<false>(dinit + p.b * d.D + p.c, s, p.n);
   // dA over the CTA's warps, in order
@@ -532,6 +573,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     for (int w = 1; w < kW; ++w) dA = dA + sums[w * 32 + p.lane];
     store2<false>(part + (p.b * p.ranks + p.rank) * d.D + p.c, dA, p.n);
   }
+  ex.finish();
 }
 
 // dA over the batch and the ranks, in order.
@@ -568,12 +610,11 @@ cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, F *f, int64
 
 // How many CTAs share a sequence: the most, up to kMaxRanks and one a tile, whose clusters the GPU holds all at once.
 // What it holds depends on how clusters of a size fill its graphics clusters (2.7B-shaped prefill, 80 blocks of
-// channels: 5 ranks 52 us, 4 60 us; 6 need a second wave, 67 us), so each kernel asks the runtime once.
+// channels: 5 ranks 47.9 us, 4 56.0 us; 6 need a second wave, 59.6 us), so each kernel asks the runtime once.
 template <typename T, int N, int kW, int kT, typename... P>
 cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) {
   static std::atomic<int> held[kMaxRanks + 1];  // clusters of each size that fit, + 1; 0: not asked yet
   ranks = (int)std::min<int64_t>((L + kW * kT - 1) / (kW * kT), kMaxRanks);
-  if (const char *e = getenv("RANKS")) { ranks = std::min(ranks, atoi(e)); return cudaSuccess; }
   for (; ranks > 1; --ranks) {
     int fit = held[ranks].load(std::memory_order_relaxed) - 1;
     if (fit < 0) {
@@ -583,7 +624,6 @@ cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) 
       if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, many, &cfg);
       if (e != cudaSuccess) return e;
       held[ranks].store(fit + 1, std::memory_order_relaxed);
-      if (getenv("GLRDBG")) printf("ranks %d fit %d\n", ranks, fit), fflush(stdout);
     }
     if (ctas <= fit) break;
   }
