@@ -129,7 +129,8 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
 // Warps, tokens a warp and CTAs an SM of each scan.  Long runs of tokens amortise a tile's exchange, small CTAs keep the
 // SMs evenly loaded (2.7B-shaped bf16 prefill: 4 x 16 47.8 us, 4 x 12 54.0, 4 x 8 54.3, 2 x 16 57.2, 8 x 16 66.5 us;
 // long-context bf16 gradient: 4 x 12 381 us, 4 x 8 408, 2 x 12 437, 4 x 4 490, 8 x 8 509 us).  fp32 tiles are twice
-// the bytes and bound by them: any of these shapes runs the same there.
+// the bytes; the prefill runs the same with any of these shapes, and the gradient's short runs leave room for four CTAs
+// (b = 4, L = 4096, D = 5120: 4 x 4 442 us, 4 x 8 507 us; b = 1, L = 16384, D = 1536: 182 and 150 us).
 template <typename T>
 struct PrefillShape {
   static constexpr int W = 4, N = sizeof(T) == 2 ? 16 : 8, kResident = 3;
@@ -185,9 +186,9 @@ struct Rows {
   __device__ __forceinline__ const T *from(int q, int64_t stride) const {
     return p + (row(q, 0) - row(0, 0)) * stride + (chan(q, 0) - chan(0, 0));
   }
-  // whole: every row and channel is there
-  __device__ __forceinline__ void fetch(T *dst, bool whole, int lo, int hi, int64_t stride, int64_t channels,
-                                        int lane) const {
+  // whole: every row and channel is there; array: where the others point instead (and nothing is read)
+  __device__ __forceinline__ void fetch(T *dst, bool whole, int lo, int hi, int64_t stride, int64_t channels, int lane,
+                                        const T *array) const {
     const uint32_t to = smem_addr(dst) + lane * E * (int)sizeof(T);
     if (CW == 16 && whole) {
 #pragma unroll
@@ -201,7 +202,7 @@ struct Rows {
       if constexpr (CW == 0)
         dst[q * 32 + lane] = valid ? *from(q, stride) : T(0.f);
       else
-        copy_async<CW>(to + q * 32 * CW, from(q, stride), valid);
+        copy_async<CW>(to + q * 32 * CW, valid ? from(q, stride) : array, valid);
     }
   }
 };
@@ -229,16 +230,13 @@ struct alignas(16) Link {
 __device__ __forceinline__ Link then(Link first, Link second) {
   return {first.A * second.A, fma2(second.A, first.H, second.H)};
 }
-constexpr int kSlots = 3;  // tiles whose messages a rank may hold
-
-// What the warps and ranks of a scan tell one another.
+// What the warps and ranks of a scan tell one another, by parity of the tile.
 template <int kW>
 struct Links {
-  Link carry[kSlots][32];  // H: the state entering the tile
   Link warp[2][kW][32];
-  uint64_t arrived[kSlots];  // mbarriers: a tile's messages from other ranks are here
-  uint64_t pad[kSlots % 2];
-  // behind it, in a cluster: Link rank[kSlots][ranks][32]
+  f2 carry[2][32];      // without a cluster: the state entering the tile
+  uint64_t arrived[2];  // in one, mbarriers: the ranks' messages of a tile are here
+  // behind it, in a cluster: Link rank[2][ranks][32]
 };
 __device__ __forceinline__ Link load_link(const Link &l) {
   const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&l);
@@ -246,49 +244,50 @@ __device__ __forceinline__ Link load_link(const Link &l) {
 }
 
 // The exchange of a tile: `publish` gives a warp's own update away, `collect` returns the state that enters its
-// tokens; every warp of every rank calls each once a tile, then `next`.  Between the ranks of a cluster the updates
-// travel as st.async messages that count themselves in on the receiver's mbarrier, so no rank waits for one behind
-// it, and no warp for its own stores to drain, as both would at a cluster barrier a tile (2.7B-shaped bf16 prefill, 5
-// ranks: 47.8 us against 52.6 us; fp32: 58 against 72 us).
-// Three slots are enough: a rank sends tile k + 3 only after it got the state that enters tile k + 2, which the last
-// rank sent after every rank had published k + 1, and so had collected k.
+// tokens, `leave` ends the tile with the state after them; every warp of every rank calls each once a tile.  In a
+// cluster every warp keeps the state that enters the tile itself, from the updates of all ranks, so no tile waits for
+// the steps of the one before; in a lone CTA its last warp hands it on.  The ranks' updates travel as st.async messages that count themselves in on the receiver's mbarrier: no warp waits
+// for its own stores to drain, as it would at a cluster barrier a tile (2.7B-shaped bf16 prefill, 5 ranks: 47.8 us
+// against 52.6 us).  Two slots are enough: a rank sends tile k + 2 after it has collected k + 1, which every rank
+// published after all its warps had collected k.
 // A wait gives up after 2 s of global time; the state is then NaN from there on.
 template <bool kCluster, int kW>
 struct Exchange {
   Links<kW> &l;
   int warp, lane, rank, ranks;
-  int par, slot, phase;  // of the tile
-  bool later, lost;      // not the first tile; a wait has expired
-  Link before;           // the warps before this one
+  int par, phase;  // of the tile
+  bool lost;       // a wait has expired
+  Link before;     // the warps before this one
+  f2 state;        // enters the tile
 
-  __device__ __forceinline__ Exchange(Links<kW> &links, int warp, int lane, int rank, int ranks)
-      : l(links), warp(warp), lane(lane), rank(rank), ranks(ranks), par(0), slot(0), phase(0), later(false), lost(false) {}
-  // The state that enters the first tile, and the barriers; then all threads of all ranks may go on.
-  __device__ __forceinline__ void start(f2 h) {
-    if (warp == 0) l.carry[0][lane].H = h;
+  // All threads of all ranks, once: `enters` the first tile.
+  __device__ __forceinline__ Exchange(Links<kW> &links, int warp, int lane, int rank, int ranks, f2 enters)
+      : l(links), warp(warp), lane(lane), rank(rank), ranks(ranks), par(0), phase(0), lost(false), state(enters) {
+    if (!kCluster && warp == 0) l.carry[0][lane] = enters;
     if constexpr (kCluster) {
       if (threadIdx.x == 0) {
-        for (int k = 0; k < kSlots; ++k) sm100::mbar_init(&l.arrived[k], 1);
+        sm100::mbar_init(&l.arrived[0], 1);
+        sm100::mbar_init(&l.arrived[1], 1);
         sm100::mbar_fence_init();
       }
       sync_ranks();
     }
   }
-  __device__ __forceinline__ Link *from_rank(int slot, int k) const {
-    return reinterpret_cast<Link *>(&l + 1) + (slot * ranks + k) * 32 + lane;
+  __device__ __forceinline__ Link *from_rank(int k) const {
+    return reinterpret_cast<Link *>(&l + 1) + (par * ranks + k) * 32 + lane;
   }
-  // One lane's 16 bytes of a message of 512.
-  __device__ __forceinline__ void send(Link *to, int slot, int rank, Link v) const {
+  // One lane's 16 bytes of this rank's message of 512 to rank k.
+  __device__ __forceinline__ void send(int k, Link v) const {
     uint32_t a, b;
     const float2 A = split(v.A), H = split(v.H);
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(to)), "r"(rank));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_addr(&l.arrived[slot])), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(from_rank(rank))), "r"(k));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_addr(&l.arrived[par])), "r"(k));
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
                  "f"(A.x), "f"(A.y), "f"(H.x), "f"(H.y), "r"(b)
                  : "memory");
   }
   __device__ __forceinline__ bool wait() const {
-    const uint32_t bar = smem_addr(&l.arrived[slot]);
+    const uint32_t bar = smem_addr(&l.arrived[par]);
     uint64_t t0 = 0;
     while (true) {
       uint32_t ok;
@@ -305,46 +304,37 @@ struct Exchange {
       if (t - t0 > 2000000000ull) return false;
     }
   }
-  __device__ __forceinline__ void prefix() {
-    before = {both(1.f), both(0.f)};
-    for (int w = 0; w < warp; ++w) before = then(before, load_link(l.warp[par][w][lane]));
-  }
   __device__ __forceinline__ void publish(Link mine) {
     l.warp[par][warp][lane] = mine;
     __syncthreads();
-    prefix();
-    if constexpr (kCluster)
+    before = {both(1.f), both(0.f)};
+    for (int w = 0; w < warp; ++w) before = then(before, load_link(l.warp[par][w][lane]));
+    if constexpr (kCluster) {
       if (warp == kW - 1) {
         const Link all = then(before, mine);
-        for (int k = rank + 1; k < ranks; ++k) send(from_rank(slot, rank), slot, k, all);
-        if (lane == 0) sm100::mbar_arrive_expect_tx(&l.arrived[slot], 512u * (rank + (later ? 1 : 0)));
+        if (lane == 0) sm100::mbar_arrive_expect_tx(&l.arrived[par], 512u * ranks);
+        for (int k = 0; k < ranks; ++k) send(k, all);
       }
+    }
   }
   __device__ __forceinline__ f2 collect() {
-    if constexpr (kCluster)
-      if (!lost) lost = !wait();
-    f2 h = l.carry[slot][lane].H;
+    f2 h = kCluster ? state : l.carry[par][lane];  // enters this CTA's tokens
     if constexpr (kCluster) {
-      for (int k = 0; k < rank; ++k) {
-        const Link f = load_link(*from_rank(slot, k));
-        h = fma2(f.A, h, f.H);
+      if (!lost) lost = !wait();
+#pragma unroll 4
+      for (int k = 0; k < ranks; ++k) {
+        const Link f = load_link(*from_rank(k));
+        if (k == rank) h = state;
+        state = fma2(f.A, state, f.H);
       }
-      if (lost) h = both(__int_as_float(0x7fffffff));
+      if (lost) h = state = both(__int_as_float(0x7fffffff));
     }
     return fma2(before.A, h, before.H);
   }
-  // To the next tile, which `h`, the state after this warp's tokens, enters if the warp is the last of the last rank.
-  __device__ __forceinline__ void next(f2 h) {
+  __device__ __forceinline__ void leave(f2 h) {
+    if (!kCluster && warp == kW - 1) l.carry[par ^ 1][lane] = h;
+    phase ^= par;
     par ^= 1;
-    later = true;
-    if (++slot == kSlots) slot = 0, phase ^= 1;
-    if (last()) {
-      const Link v = {both(0.f), h};
-      if constexpr (kCluster)
-        for (int k = 0; k < ranks; ++k) send(&l.carry[slot][lane], slot, k, v);
-      else
-        l.carry[slot][lane] = v;
-    }
   }
   __device__ __forceinline__ bool last() const { return warp == kW - 1 && rank == ranks - 1; }
   // No rank leaves while another may still write to it.
@@ -360,7 +350,7 @@ struct ScanSmem {
 };
 template <typename T, int N, int kW, int kT>
 size_t scan_smem(int ranks) {
-  return sizeof(ScanSmem<T, N, kW, kT>) + (ranks > 1 ? kSlots * ranks * 32 * sizeof(Link) : 0);
+  return sizeof(ScanSmem<T, N, kW, kT>) + (ranks > 1 ? 2 * ranks * 32 * sizeof(Link) : 0);
 }
 
 // A CTA's place in the grid.
@@ -394,7 +384,6 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 3, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 3, kW, kT> *>(raw);
   const Place p = place<kCluster>(d.D, blocks);
-  Exchange<kCluster, kW> ex(sm.links, p.warp, p.lane, p.rank, p.ranks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
   const int64_t t0 = p.rank * kTile + p.warp * kT;  // this warp's first token
@@ -408,7 +397,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
       const bool whole = p.whole && rest >= kT;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], whole, 0, (int)min(rest, (int64_t)kT), d.row, d.D - p.c0, p.lane);
+        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], whole, 0, (int)min(rest, (int64_t)kT), d.row, d.D - p.c0, p.lane,
+                      k == 0 ? x : k == 1 ? r : i);
         rows[k].p += step * d.row;
       }
     }
@@ -431,7 +421,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   };
   load(0, left);
   load(1, left - step);
-  ex.start(init != nullptr ? load_n(init + p.b * d.D + p.c, p.n) : both(0.f));
+  Exchange<kCluster, kW> ex(sm.links, p.warp, p.lane, p.rank, p.ranks,
+                            init != nullptr ? load_n(init + p.b * d.D + p.c, p.n) : both(0.f));
   T *out = h + (p.b * d.L + t0) * d.D + p.c;
   f2 s = both(0.f);
   for (int64_t tile = 0; tile < tiles; ++tile, left -= step, out += step * d.D) {
@@ -457,25 +448,44 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
         if (j < left) store2<CW == 16>(out + j * d.D, s, p.n);
       }
     }
-    if (tile + 1 < tiles) ex.next(s);
+    ex.leave(s);
   }
   if (ex.last()) store2<false>(final_state + p.b * d.D + p.c, s, p.n);
   ex.finish();
 }
 
-template <typename T>
+// One token: 4 channels a thread in wide words (kWide), else two by elements.
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, const T *__restrict__ x,
                                                     const T *__restrict__ r, const T *__restrict__ i,
                                                     const float *__restrict__ A, T *__restrict__ h, GlrDims d,
                                                     int blocks) {
-  const int64_t b = blockIdx.x / blocks, c = ((int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x) * 2;
-  const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));
+  constexpr int E = kWide ? 4 : 2;
+  const int64_t b = blockIdx.x / blocks, c = ((int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x) * E;
   const int64_t at = b * d.row + c, s = b * d.D + c;
-  f2 a, v;
-  gate(load_n(x + at, n), load_n(r + at, n), load_n(i + at, n), load_n(A + c, n), a, v);
-  const f2 next = fma2(a, load_n(state + s, n), v);
-  store2<false>(state + s, next, n);
-  store2<false>(h + s, next, n);
+  if constexpr (kWide) {
+    if (c >= d.D) return;
+    const float4 xv = load4(x + at), rv = load4(r + at), iv = load4(i + at), Av = load4(A + c), sv = load4(state + s);
+    f2 a0, v0, a1, v1;
+    gate(mk(xv.x, xv.y), mk(rv.x, rv.y), mk(iv.x, iv.y), mk(Av.x, Av.y), a0, v0);
+    gate(mk(xv.z, xv.w), mk(rv.z, rv.w), mk(iv.z, iv.w), mk(Av.z, Av.w), a1, v1);
+    v0 = fma2(a0, mk(sv.x, sv.y), v0);
+    v1 = fma2(a1, mk(sv.z, sv.w), v1);
+    const float2 lo = split(v0), hi = split(v1);
+    const float4 next = make_float4(lo.x, lo.y, hi.x, hi.y);
+    *reinterpret_cast<float4 *>(state + s) = next;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4 *>(h + s) = next;
+    else
+      *reinterpret_cast<uint2 *>(h + s) = make_uint2(to_bf16x2(v0), to_bf16x2(v1));
+  } else {
+    const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));
+    f2 a, v;
+    gate(load_n(x + at, n), load_n(r + at, n), load_n(i + at, n), load_n(A + c, n), a, v);
+    const f2 next = fma2(a, load_n(state + s, n), v);
+    store2<false>(state + s, next, n);
+    store2<false>(h + s, next, n);
+  }
 }
 
 // The reverse scan: c_t = a_t g_t with g_t = dh_t + c_{t+1}, that is c_t = a_t c_{t+1} + a_t dh_t, over
@@ -492,7 +502,6 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 5, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 5, kW, kT> *>(raw);
   const Place p = place<kCluster>(d.D, blocks);
-  Exchange<kCluster, kW> ex(sm.links, p.warp, p.lane, p.rank, p.ranks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
   // this warp's tokens are t .. t + 7; those below 0 lie before the sequence
@@ -511,7 +520,8 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
       for (int k = 0; k < 5; ++k) {
         const int64_t stride = k == 1 || k == 4 ? d.D : d.row;
         const int lo = (int)max((int64_t)0, (k == 4 ? 1 : 0) - t);
-        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], whole, lo, kT, stride, d.D - p.c0, p.lane);
+        rows[k].fetch(&sm.in[p.warp][stage][k][0][0], whole, lo, kT, stride, d.D - p.c0, p.lane,
+                      k == 0 ? r : k == 1 ? dh : k == 2 ? i : k == 3 ? x : h);
         rows[k].p -= step * stride;
       }
     }
@@ -519,7 +529,8 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   };
   load(0, t);
   load(1, t - step);
-  ex.start(dfinal != nullptr ? load_n(dfinal + p.b * d.D + p.c, p.n) : both(0.f));
+  Exchange<kCluster, kW> ex(sm.links, p.warp, p.lane, p.rank, p.ranks,
+                            dfinal != nullptr ? load_n(dfinal + p.b * d.D + p.c, p.n) : both(0.f));
   int64_t to = (p.b * d.L + t) * d.grad + p.c;
   f2 s = both(0.f), dA = both(0.f);
   for (int64_t tile = 0; tile < tiles; ++tile, t -= step, to -= step * d.grad) {
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     }
     __syncwarp();
     load(par, t - 2 * step);
-    if (tile + 1 < tiles) ex.next(s);
+    ex.leave(s);
   }
   if (dinit != nullptr && ex.last()) store2<false>(dinit + p.b * d.D + p.c, s, p.n);
   // dA over the CTA's warps, in order
@@ -574,18 +585,6 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     store2<false>(part + (p.b * p.ranks + p.rank) * d.D + p.c, dA, p.n);
   }
   ex.finish();
-}
-
-// dA over the batch and the ranks, in order.
-__global__ void __launch_bounds__(128) k_glr_sum(const float *__restrict__ part, float *__restrict__ dA, int64_t D,
-                                                 int64_t n) {
-  const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  sm100::grid_dep_wait();  // launched before the partial sums are complete
-  if (c >= D) return;
-  float s = 0.f;
-#pragma unroll 8
-  for (int64_t k = 0; k < n; ++k) s += part[k * D + c];
-  dA[c] = s;
 }
 
 bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -663,8 +662,10 @@ cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *
 template <typename T>
 cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T *i, const float *A, T *h,
                                    const GlrDims &d, cudaStream_t st) {
-  const int64_t blocks = (d.D + 255) / 256;
-  k_glr_decode<T><<<(unsigned)(blocks * d.b), 128, 0, st>>>(state, x, r, i, A, h, d, (int)blocks);
+  const bool w4 = wide(state) && wide(A) && wide(x) && wide(r) && wide(i) && wide(h) && d.D % 4 == 0 && d.row % 4 == 0;
+  const int64_t per = 128 * (w4 ? 4 : 2), blocks = (d.D + per - 1) / per;
+  auto *f = w4 ? k_glr_decode<T, true> : k_glr_decode<T, false>;
+  f<<<(unsigned)(blocks * d.b), 128, 0, st>>>(state, x, r, i, A, h, d, (int)blocks);
   return cudaGetLastError();
 }
 
@@ -691,16 +692,7 @@ cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float 
   cudaError_t e = w16 ? run(k_glr_backward<T, 16, false, W, N>, k_glr_backward<T, 16, true, W, N>)
                       : run(k_glr_backward<T, CW, false, W, N>, k_glr_backward<T, CW, true, W, N>);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((d.D + 127) / 128));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_glr_sum, (const float *)part, dA, d.D, d.b * ranks);
+  return launch_row_sums(part, nullptr, dA, nullptr, d.D, d.b * ranks, st);
 }
 
 #define SSD_GLR_INSTANCES(T)                                                                                           \

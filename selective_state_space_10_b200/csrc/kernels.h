@@ -84,6 +84,10 @@ struct NormDims {
 template <typename TX, typename TR>
 cudaError_t launch_residual_norm(const TX *x, const float *scale, const TR *res, const float *w, float eps,
                                  TR *res_out, TX *out, const NormDims &d, cudaStream_t st);
+// One or two (o1 != NULL) vectors of D as the sums of n rows each, in a fixed order; a programmatic dependent of the
+// kernel that writes the rows.
+cudaError_t launch_row_sums(const float *p0, const float *p1, float *o0, float *o1, int64_t D, int64_t n,
+                            cudaStream_t st);
 // floats of scratch: the partial sums of two vectors of dim
 size_t norm_backward_floats(const NormDims &d);
 template <typename TX, typename TR>

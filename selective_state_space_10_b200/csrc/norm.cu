@@ -515,28 +515,24 @@ __global__ void __launch_bounds__(kRowThreads)
     if (ps != nullptr) put(ss, ps);
 }
 
-// The partial sums of one or two vectors: 32 threads a column add every 32nd, then one adds those, in order.
-__global__ void __launch_bounds__(1024) k_norm_sum(const float *__restrict__ pw, const float *__restrict__ ps,
-                                                   float *dw, float *ds, int64_t D, int n) {
+// The partial sums of one or two vectors, n rows of D: 32 threads a column add every 32nd row, then a warp adds those.
+__global__ void __launch_bounds__(1024) k_row_sums(const float *__restrict__ p0, const float *__restrict__ p1,
+                                                   float *o0, float *o1, int64_t D, int64_t n) {
   __shared__ float sh[32][33];
-  const int column = threadIdx.x % 32, k = threadIdx.x / 32;
-  const int64_t c = (int64_t)blockIdx.x * 32 + column;
-  const float *p = blockIdx.y == 0 ? pw : ps;
-  float *o = blockIdx.y == 0 ? dw : ds;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t c = (int64_t)blockIdx.x * 32;
+  const float *p = blockIdx.y == 0 ? p0 : p1;
+  float *o = blockIdx.y == 0 ? o0 : o1;
   sm100::grid_dep_wait();  // launched before the partial sums are complete
   if (o == nullptr) return;
   float s = 0.f;
-  if (c < D)
+  if (c + lane < D)
 #pragma unroll 8
-    for (int j = k; j < n; j += 32) s += p[j * D + c];
-  sh[k][column] = s;
+    for (int64_t j = warp; j < n; j += 32) s += p[j * D + c + lane];
+  sh[warp][lane] = s;
   __syncthreads();
-  if (k == 0 && c < D) {
-    s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) s += sh[j][column];
-    o[c] = s;
-  }
+  s = warp_sum(sh[lane][warp], 32);
+  if (lane == 0 && c + warp < D) o[c + warp] = s;
 }
 
 int parts_of(const NormDims &d) { return (int)std::min<int64_t>(d.rows, kParts); }
@@ -654,8 +650,15 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || (dw == nullptr && ds == nullptr)) return e;
+  return launch_row_sums(pw, ps, dw, ds, d.D, parts, st);
+}
+
+}  // namespace
+
+cudaError_t launch_row_sums(const float *p0, const float *p1, float *o0, float *o1, int64_t D, int64_t n,
+                            cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((d.D + 31) / 32), ds != nullptr ? 2 : 1);
+  cfg.gridDim = dim3((unsigned)((D + 31) / 32), o1 != nullptr ? 2 : 1);
   cfg.blockDim = dim3(1024);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -663,10 +666,8 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_norm_sum, (const float *)pw, (const float *)ps, dw, ds, d.D, parts);
+  return cudaLaunchKernelEx(&cfg, k_row_sums, p0, p1, o0, o1, D, n);
 }
-
-}  // namespace
 
 size_t norm_backward_floats(const NormDims &d) { return (size_t)2 * parts_of(d) * d.D; }
 
