@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   constexpr int kTile = kW * kT;
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 3, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 3, kW, kT> *>(raw);
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
   const Place p = place<kCluster>(d.D, blocks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
@@ -461,6 +463,8 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
                                                     const float *__restrict__ A, T *__restrict__ h, GlrDims d,
                                                     int blocks) {
   constexpr int E = kWide ? 4 : 2;
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
   const int64_t b = blockIdx.x / blocks, c = ((int64_t)(blockIdx.x % blocks) * 128 + threadIdx.x) * E;
   const int64_t at = b * d.row + c, s = b * d.D + c;
   if constexpr (kWide) {
@@ -501,6 +505,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   constexpr int kTile = kW * kT;
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 5, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 5, kW, kT> *>(raw);
+  sm100::grid_dep_wait();
   const Place p = place<kCluster>(d.D, blocks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
@@ -591,17 +596,19 @@ bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // The launch of a scan kernel: `ranks` CTAs share a sequence and are a cluster.
 template <typename F>
-cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, F *f, int64_t ctas, int ranks, int warps, size_t smem,
+cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], F *f, int64_t ctas, int ranks, int warps, size_t smem,
                    cudaStream_t st) {
   cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3((unsigned)(ctas * ranks));
   cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {(unsigned)ranks, 1, 1};
-  cfg.attrs = &at;
-  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)ranks, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
@@ -618,7 +625,7 @@ cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) 
     int fit = held[ranks].load(std::memory_order_relaxed) - 1;
     if (fit < 0) {
       cudaLaunchConfig_t cfg;
-      cudaLaunchAttribute at;
+      cudaLaunchAttribute at[2];
       cudaError_t e = set_up(cfg, at, many, 1, ranks, kW, scan_smem<T, N, kW, kT>(ranks), nullptr);
       if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, many, &cfg);
       if (e != cudaSuccess) return e;
@@ -632,7 +639,7 @@ cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) 
 template <typename T, int N, int kW, int kT, typename... P, typename... V>
 cudaError_t launch_scan(void (*one)(P...), void (*many)(P...), int64_t ctas, int ranks, cudaStream_t st, V... v) {
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute at;
+  cudaLaunchAttribute at[2];
   auto *f = ranks > 1 ? many : one;
   cudaError_t e = set_up(cfg, at, f, ctas, ranks, kW, scan_smem<T, N, kW, kT>(ranks), st);
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, f, v...);
@@ -665,8 +672,7 @@ cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T
   const bool w4 = wide(state) && wide(A) && wide(x) && wide(r) && wide(i) && wide(h) && d.D % 4 == 0 && d.row % 4 == 0;
   const int64_t per = 128 * (w4 ? 4 : 2), blocks = (d.D + per - 1) / per;
   auto *f = w4 ? k_glr_decode<T, true> : k_glr_decode<T, false>;
-  f<<<(unsigned)(blocks * d.b), 128, 0, st>>>(state, x, r, i, A, h, d, (int)blocks);
-  return cudaGetLastError();
+  return launch_dependent(f, dim3((unsigned)(blocks * d.b)), 128, 0, st, state, x, r, i, A, h, d, (int)blocks);
 }
 
 size_t glr_backward_floats(const GlrDims &d) { return (size_t)d.b * kMaxRanks * d.D; }

@@ -9,6 +9,23 @@
 
 namespace ssd {
 
+// Launches f as a programmatic dependent of what the stream ran before: its CTAs take their places as the last ones of
+// that kernel leave theirs, and f itself waits (grid_dep_wait, before it touches memory) until that kernel is complete.
+template <typename... P, typename... V>
+cudaError_t launch_dependent(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, V... v) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, P(v)...);
+}
+
 // prefill_simt.cu
 cudaError_t launch_dA_cumsum(const float *dt, const float *A, float *cum, const Dims &d, int Q, int nc,
                              cudaStream_t st);

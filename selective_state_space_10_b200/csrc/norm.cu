@@ -177,6 +177,8 @@ __global__ void __launch_bounds__(row_threads(NV *VEC))
     k_norm_rows(const TX *x, const float *__restrict__ scale, const TR *wide, const float *__restrict__ w, float eps,
                 TR *wide_out, TX *out, NormDims d, int tpr, int W) {
   __shared__ float sh[32];
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
   constexpr int E = NV * VEC / 2;
   const int lane = threadIdx.x % tpr;
   const int64_t unit = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(kRowThreads)
                          int parts, int stages) {
   extern __shared__ __align__(16) char raw[];
   __shared__ f2 sh[2][32];
+  sm100::grid_dep_wait();
   using P = Pieces<M, TX, TR, VEC>;
   constexpr int E = NV * VEC / 2;
   const int lane = threadIdx.x % tpr, sub = threadIdx.x / tpr, subs = blockDim.x / tpr;
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(1024) k_row_sums(const float *__restrict__ p0,
   const int64_t c = (int64_t)blockIdx.x * 32;
   const float *p = blockIdx.y == 0 ? p0 : p1;
   float *o = blockIdx.y == 0 ? o0 : o1;
-  sm100::grid_dep_wait();  // launched before the partial sums are complete
+  sm100::grid_dep_wait();  // for the partial sums
   if (o == nullptr) return;
   float s = 0.f;
   if (c + lane < D)
@@ -563,14 +566,16 @@ Split split_unit(int64_t n, int least, int most, F limit) {
 
 template <Mode M, typename TX, typename TR, int VEC>
 bool norm_rows(const TX *x, const float *scale, const TR *wide, const float *w, float eps, TR *wide_out, TX *out,
-               const NormDims &d, cudaStream_t st) {
+               const NormDims &d, cudaError_t &err, cudaStream_t st) {
   const int64_t W = d.D / d.G;
   constexpr int least = VEC == 1 ? 2 : 1;
   const Split p = split_unit((W + VEC - 1) / VEC, least, 4 * least, [](int nv) { return row_threads(nv * VEC); });
   if (p.nv == 0) return false;
   const int threads = p.tpr <= 32 ? 128 : p.tpr, units = threads / p.tpr;
   const unsigned grid = (unsigned)((d.rows * d.G + units - 1) / units);
-  auto run = [&](auto *f) { f<<<grid, threads, 0, st>>>(x, scale, wide, w, eps, wide_out, out, d, p.tpr, (int)W); };
+  auto run = [&](auto *f) {
+    err = launch_dependent(f, grid, threads, 0, st, x, scale, wide, w, eps, wide_out, out, d, p.tpr, (int)W);
+  };
   if (p.nv == 4 * least) run(k_norm_rows<M, TX, TR, VEC, 4 * least>);
   else if (p.nv == 2 * least) run(k_norm_rows<M, TX, TR, VEC, 2 * least>);
   else run(k_norm_rows<M, TX, TR, VEC, least>);
@@ -583,9 +588,11 @@ cudaError_t norm(const TX *x, const float *scale, const TR *wide, const float *w
   constexpr int VEC = sizeof(TX) == 2 ? 8 : 4;
   const bool vec = (d.D / d.G) % VEC == 0 && d.gate % VEC == 0 && wide_ptr(x) && wide_ptr(scale) && wide_ptr(wide) &&
                    wide_ptr(w) && wide_ptr(wide_out) && wide_ptr(out);
-  if (!(vec ? norm_rows<M, TX, TR, VEC>(x, scale, wide, w, eps, wide_out, out, d, st)
-            : norm_rows<M, TX, TR, 1>(x, scale, wide, w, eps, wide_out, out, d, st)))
-    k_norm<M, TX, TR><<<(unsigned)(d.rows * d.G), kThreads, 0, st>>>(x, scale, wide, w, eps, wide_out, out, d);
+  cudaError_t err = cudaSuccess;
+  if (vec ? norm_rows<M, TX, TR, VEC>(x, scale, wide, w, eps, wide_out, out, d, err, st)
+          : norm_rows<M, TX, TR, 1>(x, scale, wide, w, eps, wide_out, out, d, err, st))
+    return err;
+  k_norm<M, TX, TR><<<(unsigned)(d.rows * d.G), kThreads, 0, st>>>(x, scale, wide, w, eps, wide_out, out, d);
   return cudaGetLastError();
 }
 
@@ -608,9 +615,8 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
   auto *f = k_norm_backward_rows<M, TX, TR, VEC, NV>;
   if (smem > 48 * 1024) err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return true;
-  f<<<(unsigned)(parts * d.G), threads, smem, st>>>(x, scale, wide, w, eps, dout, dwide, dx, dwide_out, pw, ps, d, tpr,
-                                                    (int)W, parts, stages);
-  err = cudaGetLastError();
+  err = launch_dependent(f, dim3((unsigned)(parts * d.G)), threads, smem, st, x, scale, wide, w, eps, dout, dwide, dx,
+                         dwide_out, pw, ps, d, tpr, (int)W, parts, stages);
   return true;
 }
 
@@ -657,16 +663,8 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
 
 cudaError_t launch_row_sums(const float *p0, const float *p1, float *o0, float *o1, int64_t D, int64_t n,
                             cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((D + 31) / 32), o1 != nullptr ? 2 : 1);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_row_sums, p0, p1, o0, o1, D, n);
+  return launch_dependent(k_row_sums, dim3((unsigned)((D + 31) / 32), o1 != nullptr ? 2 : 1), 1024, 0, st, p0, p1, o0,
+                          o1, D, n);
 }
 
 size_t norm_backward_floats(const NormDims &d) { return (size_t)2 * parts_of(d) * d.D; }

@@ -486,20 +486,19 @@ def _ok_f32(tensors, shape, dev: int) -> None:
             _check(t, name, shape, torch.float32, torch.device("cuda", dev))
 
 
-def _call(where: str, dev: int, stream, args) -> None:
+def _call(fn, dev: int, stream, args) -> None:
     """fn(*args, stream) on the tensors' device, on `stream` or that device's current one."""
-    fn = getattr(lib, where)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev) without its object
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
             st = fn(*args, stream)
     if st != OK:
-        raise SSDError(st, where)
+        raise SSDError(st, fn.__name__)
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -532,6 +531,10 @@ def _row_stride(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
 def _same_stride(names, x, r, i, shape, dtype, dev: int) -> int:
     """The row stride that three arrays share (any of them where there is one row at most)."""
     row = _row_stride(x, names[0], shape, dtype, dev)
+    strides = x.stride()
+    if (r.stride() == strides and i.stride() == strides and r.shape == shape and i.shape == shape and
+            r.dtype is dtype and i.dtype is dtype and r.get_device() == dev and i.get_device() == dev):
+        return row
     for name, t in ((names[1], r), (names[2], i)):
         other = _row_stride(t, name, shape, dtype, dev)
         if other != row and shape[:-1].numel() > 1:
@@ -544,8 +547,8 @@ _XRI, _GRADS = ("x", "r", "i"), ("dx", "dr", "di")
 
 def _new(like: torch.Tensor, shape, dtype) -> torch.Tensor:
     """A contiguous tensor on like's device; empty_like is the quickest way to one."""
-    if like.shape == shape and like.dtype is dtype and like.is_contiguous():
-        return torch.empty_like(like)
+    if like.shape == shape:
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
     return like.new_empty(shape, dtype=dtype)
 
 
@@ -577,7 +580,7 @@ def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream
         final_state = _new(A if initial_state is None else initial_state, (b, D), torch.float32)
     _ok_f32((("initial_state", initial_state), ("final_state", final_state)), (b, D), dev)
     dims = GlrDims(b, L, D, row, D)
-    _call("ssd_glr_prefill", dev, stream,
+    _call(lib.ssd_glr_prefill, dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
            _address(initial_state), h.data_ptr(), final_state.data_ptr()))
     return h, final_state
@@ -599,7 +602,7 @@ def glr_decode_step(state, x, r, i, A, h=None, stream=None) -> torch.Tensor:
     else:
         _ok(h, "h", shape, x.dtype, dev)
     dims = GlrDims(b, 1, D, row, D)
-    _call("ssd_glr_decode_step", dev, stream,
+    _call(lib.ssd_glr_decode_step, dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(),
            A.data_ptr(), h.data_ptr()))
     return h
@@ -631,7 +634,7 @@ def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=No
     dims = GlrDims(b, L, D, row, grad)
     need = lib.ssd_glr_backward_workspace_size(ctypes.byref(dims), _DTYPES[x.dtype])
     workspace, nbytes = _workspace(workspace, need, A)
-    _call("ssd_glr_backward", dev, stream,
+    _call(lib.ssd_glr_backward, dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
            _address(initial_state), h.data_ptr(), dh.data_ptr(), _address(dfinal_state), dx.data_ptr(),
            dr.data_ptr(), di.data_ptr(), dA.data_ptr(), dinitial_state.data_ptr(), workspace.data_ptr(), nbytes))
@@ -674,7 +677,7 @@ def residual_norm(x, weight, residual=None, scale=None, residual_dtype=None, eps
     else:
         _ok(out, "out", shape, x.dtype, dev)
     dims = NormDims(rows, D, 1, D, D)
-    _call("ssd_residual_norm", dev, stream,
+    _call(lib.ssd_residual_norm, dev, stream,
           (ctypes.byref(dims), _DTYPES[x.dtype], _DTYPES[residual_dtype], x.data_ptr(), _address(scale),
            _address(residual), weight.data_ptr(), eps, residual_out.data_ptr(), out.data_ptr()))
     return out, residual_out
@@ -713,7 +716,7 @@ def residual_norm_backward(dout, s, weight, x=None, scale=None, dresidual_out=No
     _ok_f32((("weight", weight), ("scale", scale), ("dweight", dweight), ("dscale", dscale)), (D,), dev)
     dims = NormDims(rows, D, 1, D, D)
     workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
-    _call("ssd_residual_norm_backward", dev, stream,
+    _call(lib.ssd_residual_norm_backward, dev, stream,
           (ctypes.byref(dims), _DTYPES[dout.dtype], _DTYPES[s.dtype], _address(x if scale is not None else None),
            _address(scale), s.data_ptr(), weight.data_ptr(), eps, dout.data_ptr(), _address(dresidual_out),
            dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(), _address(dscale), workspace.data_ptr(), nbytes))
@@ -739,7 +742,7 @@ def gated_norm(y, z, weight, ngroups: int = 1, gate_first: bool = True, eps: flo
     else:
         _ok(out, "out", shape, z.dtype, dev)
     dims = NormDims(rows, D, int(ngroups), gate, D)
-    _call("ssd_gated_norm", dev, stream,
+    _call(lib.ssd_gated_norm, dev, stream,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
            weight.data_ptr(), eps, out.data_ptr()))
     return out
@@ -767,7 +770,7 @@ def gated_norm_backward(dout, y, z, weight, ngroups: int = 1, gate_first: bool =
     _ok_f32((("weight", weight), ("dweight", dweight)), (D,), dev)
     dims = NormDims(rows, D, int(ngroups), gate, dgate)
     workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
-    _call("ssd_gated_norm_backward", dev, stream,
+    _call(lib.ssd_gated_norm_backward, dev, stream,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
            weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(),
            workspace.data_ptr(), nbytes))
