@@ -150,26 +150,46 @@ __device__ __forceinline__ float total(f2 v) {
 }
 
 __device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-__device__ __forceinline__ f2 from_lane(f2 v, int o) { return {__shfl_xor_sync(0xffffffffu, v.v, o)}; }
-// A sum (or a pair of them) over a unit's threads, in every one of them; sh: one a warp of the CTA, not used by the
-// call before (two buffers in turn).  kSeveral: units of several warps in one CTA, which meet at barriers of their own
-// (a kernel with numbered barriers takes all 16 of a CTA, and an SM has 64: no more than 4 CTAs fit).
-template <bool kSeveral, typename S>
-__device__ __forceinline__ S unit_sum(S v, int tpr, S *sh) {
-  for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) v = v + from_lane(v, o);
-  if (tpr <= 32) return v;
-  const int warps = tpr >> 5;
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  if constexpr (kSeveral) {
-    const int unit = threadIdx.x / tpr;
-    asm volatile("bar.sync %0, %1;" ::"r"(unit + 1), "r"(tpr) : "memory");
-    sh += unit * warps;
-  } else {
-    __syncthreads();
+
+// The sum over a unit's threads, in every one of them; sh: one float a warp.  A unit of several warps is a whole CTA.
+__device__ __forceinline__ float unit_sum(float v, int tpr, float *sh) {
+  if (tpr < 32) {
+    for (int o = tpr >> 1; o > 0; o >>= 1) v += from_lane(v, o);
+    return v;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += from_lane(v, o);
+  if (tpr == 32) return v;
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
   v = sh[0];
-  for (int j = 1; j < warps; ++j) v = v + sh[j];
+  for (int j = 1; j < (tpr >> 5); ++j) v += sh[j];
   return v;
+}
+
+// Two sums; sh: a pair a warp of the CTA, not used by the call before (two buffers in turn).  The units of several
+// warps that share a CTA meet at barriers of their own (a kernel with numbered barriers takes all 16 of a CTA, and an SM
+// has 64: no more than 4 CTAs fit).  Half a warp adds up each sum: one exchange in place of one for each.
+__device__ __forceinline__ float2 unit_sums(float a, float b, int tpr, f2 *sh) {
+  if (tpr < 32) {
+    for (int o = tpr >> 1; o > 0; o >>= 1) a += from_lane(a, o), b += from_lane(b, o);
+    return make_float2(a, b);
+  }
+  const bool upper = threadIdx.x & 16;
+  float v = upper ? b : a;
+  v += from_lane(upper ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += from_lane(v, o);
+  if (tpr == 32) return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+  const int warps = tpr >> 5, unit = tpr == blockDim.x ? 0 : threadIdx.x / tpr;
+  if ((threadIdx.x & 15) == 0) reinterpret_cast<float *>(sh)[threadIdx.x >> 4] = v;
+  if (tpr == blockDim.x)
+    __syncthreads();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(unit + 1), "r"(tpr) : "memory");
+  f2 s = sh[unit * warps];
+  for (int j = 1; j < warps; ++j) s = s + sh[unit * warps + j];
+  return split(s);
 }
 
 template <Mode M, typename TX, typename TR, int VEC, int NV>
@@ -223,7 +243,7 @@ __global__ void __launch_bounds__(row_threads(NV *VEC))
   f2 ss = both(0.f);
 #pragma unroll
   for (int e = 0; e < E; ++e) ss = fma2(v[e], v[e], ss);
-  const f2 rstd = both(rsqrtf(unit_sum<false>(total(ss), tpr, sh) / (float)W + eps));
+  const f2 rstd = both(rsqrtf(unit_sum(total(ss), tpr, sh) / (float)W + eps));
   if (M == kResidual && wide_out != nullptr) store_runs<TR, VEC, NV>(wide_out + row * d.D + c0, at, on, v);
   Runs<float, VEC, NV> rg;
   rg.load(w + c0, at);
@@ -342,9 +362,11 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int E = NV * VEC / 2;
   const int lane = threadIdx.x % tpr, sub = threadIdx.x / tpr, subs = blockDim.x / tpr;
   const int part = blockIdx.x % parts, c0 = blockIdx.x / parts * W;
-  const int64_t step = (int64_t)parts * subs, first = (int64_t)part * subs;
-  const int64_t turns = (d.rows - first + step - 1) / step;  // the same for all of the CTA
-  const int64_t xs = M == kResidual ? d.D : d.gate;
+  const unsigned rows = (unsigned)d.rows, step = parts * subs, first = part * subs;  // rows < 2^31
+  const int turns = (int)((rows - first + step - 1) / step);                          // the same for all of the CTA
+  const int D = (int)d.D;
+  const int64_t xs = M == kResidual ? D : d.gate;
+  const float per = 1.f / (float)W;
   const bool want_x = M != kResidual || ps != nullptr, want_d = M == kResidual && dwide != nullptr;
   int at[NV];
   bool in[NV];
@@ -359,11 +381,13 @@ __global__ void __launch_bounds__(kRowThreads)
   const bool scaled = M == kResidual && scale != nullptr;
   uint4 *ring = reinterpret_cast<uint4 *>(raw) + threadIdx.x;
   uint4 *mine = ring + stages * stage_pitch;  // this thread's weights (and scales), behind the ring
-  auto fetch = [&](int64_t turn, int stage) {
+  unsigned ahead = first + sub;  // the next row to fetch
+  auto fetch = [&](int stage) {
     if constexpr (VEC > 1) {
-      const int64_t row = first + turn * step + sub;
-      if (turn < turns && row < d.rows) {
-        const int64_t o = row * d.D + c0;
+      const unsigned row = ahead;
+      ahead = min(ahead + step, 0x80000000u);
+      if (row < rows) {
+        const int64_t o = (int64_t)row * D + c0;
         uint4 *slot = ring + stage * stage_pitch;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -398,11 +422,11 @@ __global__ void __launch_bounds__(kRowThreads)
     sw[e] = both(0.f);
     if (M == kResidual) ss[e] = both(0.f);
   }
-  for (int s = 0; s < stages; ++s) fetch(s, s);
+  for (int s = 0; s < stages; ++s) fetch(s);
   int stage = 0;
-  for (int64_t turn = 0; turn < turns; ++turn) {
-    const int64_t row = first + turn * step + sub;
-    const bool live = row < d.rows;
+  unsigned row = first + sub;
+  for (int turn = 0; turn < turns; ++turn, row += step) {
+    const bool live = row < rows;
     bool on[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) on[k] = live && in[k];
@@ -417,7 +441,8 @@ __global__ void __launch_bounds__(kRowThreads)
       if constexpr (VEC > 1) runs.load_pieces(slot + piece * pitch, P::all, pitch);
       else runs.load(p, at);
     };
-    const int64_t r = live ? row : 0, ro = r * d.D + c0;
+    const unsigned r = live ? row : 0;
+    const int64_t ro = (int64_t)r * D + c0;
     // v: what is normed; uw: the gradient of the weighted norm times the weight
     f2 v[E], uw[E], s0 = both(0.f), s1 = both(0.f);
     {
@@ -448,10 +473,10 @@ __global__ void __launch_bounds__(kRowThreads)
       s0 = fma2(v[e], v[e], s0);
       s1 = fma2(uw[e], v[e], s1);
     }
-    const float2 sums = split(unit_sum<true>(mk(total(s0), total(s1)), tpr, sh[turn & 1]));
+    const float2 sums = unit_sums(total(s0), total(s1), tpr, sh[turn & 1]);
     if (live) {  // nothing was fetched for a row past the last one
-      const float rs1 = rsqrtf(sums.x / (float)W + eps);
-      const f2 rstd = both(rs1), mean = both(-sums.y * rs1 / (float)W);
+      const float rs1 = rsqrtf(fmaf(sums.x, per, eps));
+      const f2 rstd = both(rs1), mean = both(-sums.y * rs1 * per);
       Runs<TX, VEC, NV> rdout, rx;
       f2 a[E];
       take(rdout, P::dout, dout + ro);
@@ -491,10 +516,10 @@ __global__ void __launch_bounds__(kRowThreads)
           }
         }
       }
-      if (dx != nullptr) store_runs<TX, VEC, NV>(dx + row * (M == kResidual ? d.D : d.dgate) + c0, at, on, a);
+      if (dx != nullptr) store_runs<TX, VEC, NV>(dx + row * (M == kResidual ? (int64_t)D : d.dgate) + c0, at, on, a);
       if (dwide_out != nullptr) store_runs<TR, VEC, NV>(dwide_out + ro, at, on, v);
     }
-    fetch(turn + stages, stage);
+    fetch(stage);
     stage = stage + 1 == stages ? 0 : stage + 1;
   }
   // the CTA's sums: over its units in order, through shared memory where there are several
