@@ -337,7 +337,10 @@ __device__ __forceinline__ void wait_async(int left) {  // at most `left` (0 .. 
 }
 
 constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory, all its CTAs together
-constexpr int kRowThreads = 640;        // of an SM, all its CTAs together: 96 registers each
+// Threads of an SM, all its CTAs together, which leaves each 80 registers (43690 x 768 bf16 beside fp32, gated and
+// residual: 96 and 118 us; 640 threads 102 and 123, 896 threads 97 and 119; at 2560 and 5120 channels 640 and 768 run
+// alike, 896 up to 15 % longer).
+constexpr int kRowThreads = 768;
 
 // 16-byte pieces of a run of VEC channels of the four inputs, and of an fp32 vector
 template <Mode M, typename TX, typename TR, int VEC>
@@ -638,7 +641,7 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
   const int stages = VEC > 1 ? std::max(1, std::min(4, (kRingBytes / resident - fixed) / stage)) : 1;
   const size_t smem = std::max((size_t)stages * stage + fixed, (size_t)threads * VEC * NV * 4);
   auto *f = k_norm_backward_rows<M, TX, TR, VEC, NV>;
-  if (smem > 48 * 1024) err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return true;
   err = launch_dependent(f, dim3((unsigned)(parts * d.G)), threads, smem, st, x, scale, wide, w, eps, dout, dwide, dx,
                          dwide_out, pw, ps, d, tpr, (int)W, parts, stages);
@@ -661,8 +664,8 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
         x, scale, wide, w, eps, dout, dwide, dx, dwide_out, pw, ps, d, parts, e, st);
   };
   // 8 or 16 channels a thread.  The residual norm's two vectors of sums fill the registers at 8 (65536 x 768, bf16
-  // with an fp32 stream: 200 us, at 16 330); the gated norm's one leaves room for 16, and half the reductions a row
-  // (4096 x 5120: 78 us, at 8 92), unless more lanes are left idle than at 8 (43690 x 768: 136 us, at 8 111).  Rows
+  // with an fp32 stream: 195 us, at 16 330); the gated norm's one leaves room for 16, and half the reductions a row
+  // (4096 x 5120: 71 us, at 8 92), unless more lanes are left idle than at 8 (43690 x 768: 136 us, at 8 96).  Rows
   // too long for 8 take 16 in any case.
   const int64_t W = d.D / d.G;
   auto idle = [&](int n) {

@@ -1,6 +1,9 @@
 """GPU parity of the gated linear recurrence and the norms with the fp64 oracle
 (oracle/block.py), within the error bounds that the oracle carries for fp32 arithmetic plus
 one rounding to the output's type (at most eps / 2 of the value)."""
+import os
+import subprocess
+import sys
 import zlib
 
 import numpy as np
@@ -237,6 +240,16 @@ def test_norms_of_zero_and_tiny_and_large_rows(ssd):
         y[1, 5] = inf
         got = ssd.gated_norm(y, torch.ones_like(y), w)
         assert torch.isfinite(got[[0, 2]]).all() and not torch.isfinite(got[1]).all()
+
+
+def test_first_gradient_of_a_process():
+    """A kernel's shared memory is asked for before its first launch, not left from a larger call: 1536 fp32 channels
+    take 48 KB of it beside the kernel's own."""
+    code = ("import torch; from selective_state_space_10_b200 import ssd; y = torch.ones(9, 1536, device='cuda'); "
+            "w = torch.ones(1536, device='cuda'); ssd.gated_norm_backward(y, y, y, w); torch.cuda.synchronize()")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_norms_of_no_rows(ssd):
