@@ -370,6 +370,8 @@ SSD_API ssd_status ssd_decode_window_flush(const ssd_dims *dims, ssd_dtype dtype
  * formed from expm1(L), so decays close to 1 lose nothing.  Arrays need only the
  * alignment of their elements; the wide-load path is taken when x, r, i, h (and their
  * gradients) are 16-byte aligned and dim and the strides are multiples of 16 bytes.
+ * CTAs that share a long sequence wait for one another's part of a tile for at most 2 s;
+ * after a wait that expired the channels concerned hold NaN from that tile on.
  */
 typedef struct {
   int64_t batch;       /* >= 0                                                           */

@@ -141,6 +141,7 @@ struct BackwardShape {
 };
 constexpr int kCh = 64;  // channels a CTA
 constexpr int kMaxRanks = 16;
+constexpr int64_t kMaxCtas = 148 * 4;  // of a launch whose CTAs share sequences
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -614,7 +615,8 @@ cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], F *f, 
   return e;
 }
 
-// How many CTAs share a sequence: the most, up to kMaxRanks and one a tile, whose clusters the GPU holds all at once.
+// How many CTAs share a sequence: the most, up to kMaxRanks, one a tile and kMaxCtas in all, whose clusters the GPU
+// holds at once.
 // What it holds depends on how clusters of a size fill its graphics clusters (2.7B-shaped prefill, 80 blocks of
 // channels: 5 ranks 47.9 us, 4 56.0 us; 6 need a second wave, 59.6 us), so each kernel asks the runtime once.
 template <typename T, int N, int kW, int kT, typename... P>
@@ -622,6 +624,7 @@ cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) 
   static std::atomic<int> held[kMaxRanks + 1];  // clusters of each size that fit, + 1; 0: not asked yet
   ranks = (int)std::min<int64_t>((L + kW * kT - 1) / (kW * kT), kMaxRanks);
   for (; ranks > 1; --ranks) {
+    if (ctas * ranks > kMaxCtas) continue;
     int fit = held[ranks].load(std::memory_order_relaxed) - 1;
     if (fit < 0) {
       cudaLaunchConfig_t cfg;
@@ -675,7 +678,8 @@ cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T
   return launch_dependent(f, dim3((unsigned)(blocks * d.b)), 128, 0, st, state, x, r, i, A, h, d, (int)blocks);
 }
 
-size_t glr_backward_floats(const GlrDims &d) { return (size_t)d.b * kMaxRanks * d.D; }
+// A row of dim for each batch row and rank, of which there are at most kMaxCtas blocks of kCh where ranks > 1.
+size_t glr_backward_floats(const GlrDims &d) { return (size_t)std::max(d.b * d.D, kMaxCtas * kCh); }
 
 template <typename T>
 cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float *A, const float *init, const T *h,

@@ -60,7 +60,8 @@ def _decays(gen, D):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 8), (2, 5, 3), (3, 64, 64), (1, 65, 72), (2, 127, 130), (1, 700, 8), (1, 2100, 200),
-          (4, 33, 520), (1, 4097, 64), (5, 2, 1000)]
+          (4, 33, 520), (1, 4097, 64), (5, 2, 1000),
+          (700, 3, 64), (40, 100, 1024)]
 
 
 @pytest.mark.parametrize("layout", ["own", "sliced", "odd"])
@@ -333,6 +334,77 @@ def test_on_a_side_stream_and_in_graphs(ssd):
         torch.cuda.synchronize()
         for out, new in zip(outs, order):
             assert all(torch.equal(a, b) for a, b in zip(out, want[id(new)]))
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """No call needs an eager one before it: launch set-up and queries are allowed during capture."""
+    code = """
+import torch
+from selective_state_space_10_b200 import ssd
+x = torch.randn(2, 700, 128, device='cuda', dtype=torch.bfloat16); y = torch.randn(2, 700, 128, device='cuda')
+w = torch.ones(128, device='cuda')
+def run():
+    h, s = ssd.glr_prefill(x, x, x, -w)
+    g = ssd.glr_backward(x, x, x, -w, h, x, None, s)
+    out, r = ssd.residual_norm(x, w, residual=y, scale=w)
+    b = ssd.residual_norm_backward(x, r, w, x=x, scale=w)
+    return [h, s, out, r, ssd.gated_norm(y, x, w), ssd.glr_decode_step(s.clone(), x[:, 0], x[:, 1], x[:, 2], -w), *g, *b,
+            *ssd.gated_norm_backward(x, y, x, w)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_outputs_not_wanted(ssd):
+    """NULL for an optional array of the C calls leaves the others as they are with it."""
+    gen, null = _gen(19), None
+    rows, D = 37, 512
+    x, y, dout, res = (_rand(gen, rows, D) for _ in range(4))
+    w, sc = 1 + _rand(gen, D, std=0.1), _rand(gen, D)
+    st = torch.cuda.current_stream().cuda_stream
+    dims = ssd.NormDims(rows, D, 2, D, D)
+    out, s = ssd.residual_norm(x, w, residual=res, scale=sc)
+    only = torch.empty_like(out)
+    assert ssd.lib.ssd_residual_norm(dims, 0, 0, x.data_ptr(), sc.data_ptr(), res.data_ptr(), w.data_ptr(), EPS, null,
+                                     only.data_ptr(), st) == ssd.OK
+    assert torch.equal(only, out)
+    need = ssd.lib.ssd_norm_backward_workspace_size(dims)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = ssd.residual_norm_backward(dout, s, w, x=x, scale=sc, dresidual_out=res)
+    gates = ssd.gated_norm_backward(dout, y, x, w, ngroups=2)
+    for k in range(4):
+        got = [torch.full_like(t, 7.0) for t in want]
+        p = [null if j == k else t.data_ptr() for j, t in enumerate(got)]
+        assert ssd.lib.ssd_residual_norm_backward(dims, 0, 0, x.data_ptr() if k != 3 else null, sc.data_ptr(),
+                                                  s.data_ptr(), w.data_ptr(), EPS, dout.data_ptr(), res.data_ptr(), *p,
+                                                  ws.data_ptr(), need, st) == ssd.OK
+        for j, t in enumerate(got):
+            assert (t == 7).all() if j == k else torch.equal(t, want[j])
+        if k < 3:
+            got = [torch.full_like(t, 7.0) for t in gates]
+            p = [null if j == k else t.data_ptr() for j, t in enumerate(got)]
+            assert ssd.lib.ssd_gated_norm_backward(dims, 0, 0, 1, y.data_ptr(), x.data_ptr(), w.data_ptr(), EPS,
+                                                   dout.data_ptr(), *p, ws.data_ptr(), need, st) == ssd.OK
+            for j, t in enumerate(got):
+                assert (t == 7).all() if j == k else torch.equal(t, gates[j])
+    v = [t[None] for t in (x, y, dout)]
+    h, _ = ssd.glr_prefill(*v, -w.abs())
+    want = ssd.glr_backward(*v, -w.abs(), h, v[0])
+    got = [torch.empty_like(t) for t in want[:4]]
+    gd = ssd.GlrDims(1, rows, D, D, D)
+    need = ssd.lib.ssd_glr_backward_workspace_size(gd, 0)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    A = -w.abs()
+    assert ssd.lib.ssd_glr_backward(gd, 0, *(t.data_ptr() for t in v), A.data_ptr(), null, h.data_ptr(), v[0].data_ptr(),
+                                    null, *(t.data_ptr() for t in got), null, ws.data_ptr(), need, st) == ssd.OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_explicit_stream_argument(ssd):
