@@ -5,6 +5,7 @@
 // over whole sequences, for one token, and its gradients.
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -102,7 +103,7 @@ template <typename T>
 __device__ __forceinline__ f2 load_n(const T *p, int n) {
   return mk(n > 0 ? to_f32(p[0]) : 0.f, n > 1 ? to_f32(p[1]) : 0.f);
 }
-// Out; kPair: the address is aligned for both and n is 0 or 2.
+// Out; kPair: the address is aligned for both, and n is 0 or 2.
 template <bool kPair, typename T>
 __device__ __forceinline__ void store2(T *p, f2 f, int n) {
   const float2 s = split(f);
@@ -442,13 +443,13 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
 #pragma unroll
       for (int j = 0; j < kT; ++j) {
         s = fma2(a[j], s, v[j]);
-        store2<CW == 16>(out + j * d.D, s, p.n);
+        store2<(CW >= 2 * (int)sizeof(T))>(out + j * d.D, s, p.n);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < kT; ++j) {
         s = fma2(a[j], s, v[j]);
-        if (j < left) store2<CW == 16>(out + j * d.D, s, p.n);
+        if (j < left) store2<(CW >= 2 * (int)sizeof(T))>(out + j * d.D, s, p.n);
       }
     }
     ex.leave(s);
@@ -570,9 +571,9 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
       slopes(Ac, a[j], v[j], load2(&in[0][j][2 * p.lane]), load2(&in[2][j][2 * p.lane]), load2(&in[3][j][2 * p.lane]),
              before, load2(&in[1][j][2 * p.lane]), s, ox, orr, oi, dA);
       if (t + j >= 0) {
-        store2<CW == 16>(dx + to + j * d.grad, ox, p.n);
-        store2<CW == 16>(dr + to + j * d.grad, orr, p.n);
-        store2<CW == 16>(di + to + j * d.grad, oi, p.n);
+        store2<(CW >= 2 * (int)sizeof(T))>(dx + to + j * d.grad, ox, p.n);
+        store2<(CW >= 2 * (int)sizeof(T))>(dr + to + j * d.grad, orr, p.n);
+        store2<(CW >= 2 * (int)sizeof(T))>(di + to + j * d.grad, oi, p.n);
       }
     }
     __syncwarp();
@@ -593,6 +594,17 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   ex.finish();
 }
 
+// Bytes of a copy that every array's rows allow: 16, 4, or 0 (elements of 2).  2.7B-shaped bf16 prefill: 47 us with 16;
+// two channels more, 62 us with 4; one more, 97 us by elements.
+template <typename T>
+int copy_width(std::initializer_list<const void *> arrays, std::initializer_list<int64_t> strides) {
+  int width = 16;
+  for (const void *p : arrays)
+    while (width > 0 && reinterpret_cast<uintptr_t>(p) % width != 0) width = width == 16 ? 4 : 0;
+  for (int64_t s : strides)
+    while (width > 0 && s * (int64_t)sizeof(T) % width != 0) width = width == 16 ? 4 : 0;
+  return width;
+}
 bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // The launch of a scan kernel: `ranks` CTAs share a sequence and are a cluster.
@@ -654,8 +666,7 @@ template <typename T>
 cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h,
                                float *final_state, const GlrDims &d, cudaStream_t st) {
   const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
-  constexpr int E = 16 / sizeof(T);
-  const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && d.D % E == 0 && d.row % E == 0;
+  const int width = copy_width<T>({x, r, i, h}, {d.D, d.row});
   using Shape = PrefillShape<T>;
   constexpr int W = Shape::W, N = Shape::N;
   auto run = [&](auto *one, auto *many) {
@@ -664,9 +675,12 @@ cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *
     if (e != cudaSuccess) return e;
     return launch_scan<T, 3, W, N>(one, many, ctas, ranks, st, x, r, i, A, init, h, final_state, d, (int)blocks);
   };
-  if (w16) return run(k_glr_prefill<T, 16, false, W, N>, k_glr_prefill<T, 16, true, W, N>);
-  constexpr int CW = sizeof(T) == 4 ? 4 : 0;
-  return run(k_glr_prefill<T, CW, false, W, N>, k_glr_prefill<T, CW, true, W, N>);
+  switch (width) {
+    case 16: return run(k_glr_prefill<T, 16, false, W, N>, k_glr_prefill<T, 16, true, W, N>);
+    case 4: return run(k_glr_prefill<T, 4, false, W, N>, k_glr_prefill<T, 4, true, W, N>);
+  }
+  if constexpr (sizeof(T) == 2) return run(k_glr_prefill<T, 0, false, W, N>, k_glr_prefill<T, 0, true, W, N>);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>
@@ -686,9 +700,7 @@ cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float 
                                 const T *dh, const float *dfinal, T *dx, T *dr, T *di, float *dA, float *dinit,
                                 float *part, const GlrDims &d, cudaStream_t st) {
   const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
-  constexpr int E = 16 / sizeof(T);
-  const bool w16 = wide(x) && wide(r) && wide(i) && wide(h) && wide(dh) && wide(dx) && wide(dr) && wide(di) &&
-                   d.D % E == 0 && d.row % E == 0 && d.grad % E == 0;
+  const int width = copy_width<T>({x, r, i, h, dh, dx, dr, di}, {d.D, d.row, d.grad});
   using Shape = BackwardShape<T>;
   constexpr int W = Shape::W, N = Shape::N;
   int ranks = 1;
@@ -698,9 +710,10 @@ cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float 
     return launch_scan<T, 5, W, N>(one, many, ctas, ranks, st, x, r, i, A, init, h, dh, dfinal, dx, dr, di, dinit, part, d,
                                    (int)blocks);
   };
-  constexpr int CW = sizeof(T) == 4 ? 4 : 0;
-  cudaError_t e = w16 ? run(k_glr_backward<T, 16, false, W, N>, k_glr_backward<T, 16, true, W, N>)
-                      : run(k_glr_backward<T, CW, false, W, N>, k_glr_backward<T, CW, true, W, N>);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (width == 16) e = run(k_glr_backward<T, 16, false, W, N>, k_glr_backward<T, 16, true, W, N>);
+  else if (width == 4) e = run(k_glr_backward<T, 4, false, W, N>, k_glr_backward<T, 4, true, W, N>);
+  else if constexpr (sizeof(T) == 2) e = run(k_glr_backward<T, 0, false, W, N>, k_glr_backward<T, 0, true, W, N>);
   if (e != cudaSuccess) return e;
   return launch_row_sums(part, nullptr, dA, nullptr, d.D, d.b * ranks, st);
 }

@@ -66,7 +66,7 @@ SHAPES = [(1, 1, 1), (1, 1, 8), (2, 5, 3), (3, 64, 64), (1, 65, 72), (2, 127, 13
 
 @pytest.mark.parametrize("layout", ["own", "sliced", "odd"])
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
-@pytest.mark.parametrize("b,L,D", SHAPES)
+@pytest.mark.parametrize("b,L,D", SHAPES + [(2, 300, 74)])
 def test_glr_prefill_and_backward(ssd, b, L, D, dtype, layout):
     gen = _gen(b, L, D, layout)
     x, r, i = _wide(gen, b, L, D, dtype, layout)
