@@ -1,4 +1,5 @@
-"""libssd: the Mamba-2 SSD layer (chunked prefill + O(1) cached decode) for B200.
+"""libssd: the Mamba-2 SSD layer (chunked prefill + O(1) cached decode), a gated linear
+recurrence and the norms around either mixer, with the gradients of these, for B200.
 
 The compute path is the C-ABI shared library `libssd.so` built from `csrc/`; `ssd` is
 its thin Python binding (argument marshalling only).  Importing the package does not

@@ -377,6 +377,11 @@ __device__ __forceinline__ Place place(int64_t D, int blocks) {
   return p;
 }
 
+// The forward scan.  2.7B-shaped bf16 layer (b = 1, L = 4096, D = 5120): 47.4 us for 168 MB, 3.5 TB/s, 54 % of the
+// measured copy bandwidth; fp32 57.5 us, 5.8 TB/s.  The bf16 scan has twice the elements a byte: 35 warp instructions and
+// 4 special functions for each, issue slots 50 % and special-function units 46 % busy with the 10 warps an SM that 160
+// registers leave; what remains is their latency.  Forming the next tile's gates while a tile's exchange is under way
+// (a second set of registers, 8 warps an SM) measured 64 us.
 template <typename T, int CW, bool kCluster, int kW, int kT>
 __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
     k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
@@ -458,7 +463,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   ex.finish();
 }
 
-// One token: 4 channels a thread in wide words (kWide), else two by elements.
+// One token: 4 channels a thread in wide words (kWide), else two by elements.  256 x 5120 bf16 (21 MB, inside L2): 5.1 us
+// on the device, 7.2 us by elements; a call takes the host longer than that.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, const T *__restrict__ x,
                                                     const T *__restrict__ r, const T *__restrict__ i,
@@ -495,9 +501,9 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
 }
 
 // The reverse scan: c_t = a_t g_t with g_t = dh_t + c_{t+1}, that is c_t = a_t c_{t+1} + a_t dh_t, over
-// tiles from the sequence's end.  Of the gates only the decay is needed before the barrier; it is kept,
-// and the rest is formed when g is known.  A tile is 5 inputs deep, which leaves two CTAs an SM for bf16
-// and one for fp32.
+// tiles from the sequence's end.  Of the gates only the decay is needed before the exchange; it is kept,
+// and the rest is formed when g is known.  Long-context bf16 batch (b = 4, L = 16384, D = 1536): 371 us for
+// 1.61 GB, 4.3 TB/s, 66 % of the measured copy bandwidth; issue slots 53 % busy, as in the forward scan.
 template <typename T, int CW, bool kCluster, int kW, int kT>
 __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     k_glr_backward(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
