@@ -486,12 +486,9 @@ def _ok_f32(tensors, shape, dev: int) -> None:
             _check(t, name, shape, torch.float32, torch.device("cuda", dev))
 
 
-def _call(fn, dev: int, stream, args) -> None:
-    """fn(*args, stream) on the tensors' device, on `stream` or that device's current one."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev) without its object
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
+def _call(fn, dev: int, args) -> None:
+    """fn(*args, stream) on the tensors' device and that device's current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev) without its object
     if dev == torch._C._cuda_getDevice():
         st = fn(*args, stream)
     else:
@@ -499,6 +496,15 @@ def _call(fn, dev: int, stream, args) -> None:
             st = fn(*args, stream)
     if st != OK:
         raise SSDError(st, fn.__name__)
+
+
+def _on(stream, like: torch.Tensor, fn, *args):
+    """fn(*args) with `stream` (a torch stream or a handle) current, so that what fn allocates
+    is that stream's memory too: nothing of it is reused before the stream has passed the call."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -565,6 +571,8 @@ def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream
     a_t = exp(A sigmoid(r_t)), over x, r, i [b, L, D] (fp32 or bf16; they may be column slices of one array)
     and A [D] fp32 (<= 0), from initial_state [b, D] fp32 (None: zero).  Returns (h [b, L, D] in x's dtype,
     final_state [b, D] fp32); final_state may be initial_state."""
+    if stream is not None:
+        return _on(stream, x, glr_prefill, x, r, i, A, initial_state, h, final_state)
     if x.dim() != 3:
         raise ValueError("x, r and i must be [b,L,D]")
     dev = _cuda(x, "x")
@@ -580,7 +588,7 @@ def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream
         final_state = _new(A if initial_state is None else initial_state, (b, D), torch.float32)
     _ok_f32((("initial_state", initial_state), ("final_state", final_state)), (b, D), dev)
     dims = GlrDims(b, L, D, row, D)
-    _call(lib.ssd_glr_prefill, dev, stream,
+    _call(lib.ssd_glr_prefill, dev,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
            _address(initial_state), h.data_ptr(), final_state.data_ptr()))
     return h, final_state
@@ -589,6 +597,8 @@ def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream
 def glr_decode_step(state, x, r, i, A, h=None, stream=None) -> torch.Tensor:
     """ssd_glr_decode_step: one token of every sequence.  Updates `state` [b, D] fp32 in place and returns h
     [b, D]; x, r, i [b, D] as for glr_prefill (their rows may be slices)."""
+    if stream is not None:
+        return _on(stream, x, glr_decode_step, state, x, r, i, A, h)
     if x.dim() != 2:
         raise ValueError("x, r and i must be [b,D]")
     dev = _cuda(x, "x")
@@ -602,7 +612,7 @@ def glr_decode_step(state, x, r, i, A, h=None, stream=None) -> torch.Tensor:
     else:
         _ok(h, "h", shape, x.dtype, dev)
     dims = GlrDims(b, 1, D, row, D)
-    _call(lib.ssd_glr_decode_step, dev, stream,
+    _call(lib.ssd_glr_decode_step, dev,
           (ctypes.byref(dims), _DTYPES[x.dtype], state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(),
            A.data_ptr(), h.data_ptr()))
     return h
@@ -613,6 +623,9 @@ def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=No
     """ssd_glr_backward: gradients of glr_prefill from its inputs, its output h, and the gradients dh of h
     and dfinal_state of the final state (None: zero).  Returns (dx, dr, di, dA, dinitial_state); dx, dr and di
     given by the caller may be column slices of one array."""
+    if stream is not None:
+        return _on(stream, x, glr_backward, x, r, i, A, h, dh, initial_state, dfinal_state, dx, dr, di, dA,
+                   dinitial_state, workspace)
     if x.dim() != 3:
         raise ValueError("x, r and i must be [b,L,D]")
     dev = _cuda(x, "x")
@@ -634,7 +647,7 @@ def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=No
     dims = GlrDims(b, L, D, row, grad)
     need = lib.ssd_glr_backward_workspace_size(ctypes.byref(dims), _DTYPES[x.dtype])
     workspace, nbytes = _workspace(workspace, need, A)
-    _call(lib.ssd_glr_backward, dev, stream,
+    _call(lib.ssd_glr_backward, dev,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
            _address(initial_state), h.data_ptr(), dh.data_ptr(), _address(dfinal_state), dx.data_ptr(),
            dr.data_ptr(), di.data_ptr(), dA.data_ptr(), dinitial_state.data_ptr(), workspace.data_ptr(), nbytes))
@@ -656,6 +669,8 @@ def residual_norm(x, weight, residual=None, scale=None, residual_dtype=None, eps
     s / sqrt(mean(s^2) + eps) * weight over the last axis.  x [..., D] fp32 or bf16; residual in x's dtype or
     fp32; weight, scale [D] fp32.  Returns (out in x's dtype, s in residual_dtype: residual's, else x's);
     residual_out may be residual."""
+    if stream is not None:
+        return _on(stream, x, residual_norm, x, weight, residual, scale, residual_dtype, eps, residual_out, out)
     dev = _cuda(x, "x")
     shape = x.shape
     rows, D = _norm_rows(x, "x")
@@ -677,7 +692,7 @@ def residual_norm(x, weight, residual=None, scale=None, residual_dtype=None, eps
     else:
         _ok(out, "out", shape, x.dtype, dev)
     dims = NormDims(rows, D, 1, D, D)
-    _call(lib.ssd_residual_norm, dev, stream,
+    _call(lib.ssd_residual_norm, dev,
           (ctypes.byref(dims), _DTYPES[x.dtype], _DTYPES[residual_dtype], x.data_ptr(), _address(scale),
            _address(residual), weight.data_ptr(), eps, residual_out.data_ptr(), out.data_ptr()))
     return out, residual_out
@@ -688,6 +703,9 @@ def residual_norm_backward(dout, s, weight, x=None, scale=None, dresidual_out=No
     """ssd_residual_norm_backward: gradients of residual_norm from dout, the sum `s` it returned, and the
     gradient dresidual_out of that sum (None: zero); x is needed with a scale.  Returns (dx, dresidual,
     dweight, dscale), dscale None without a scale; dresidual may be dresidual_out."""
+    if stream is not None:
+        return _on(stream, dout, residual_norm_backward, dout, s, weight, x, scale, dresidual_out, eps, dx,
+                   dresidual, dweight, dscale, workspace)
     dev = _cuda(dout, "dout")
     if s.dtype not in _DTYPES:
         raise ValueError(f"unsupported s dtype {s.dtype}")
@@ -716,7 +734,7 @@ def residual_norm_backward(dout, s, weight, x=None, scale=None, dresidual_out=No
     _ok_f32((("weight", weight), ("scale", scale), ("dweight", dweight), ("dscale", dscale)), (D,), dev)
     dims = NormDims(rows, D, 1, D, D)
     workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
-    _call(lib.ssd_residual_norm_backward, dev, stream,
+    _call(lib.ssd_residual_norm_backward, dev,
           (ctypes.byref(dims), _DTYPES[dout.dtype], _DTYPES[s.dtype], _address(x if scale is not None else None),
            _address(scale), s.data_ptr(), weight.data_ptr(), eps, dout.data_ptr(), _address(dresidual_out),
            dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(), _address(dscale), workspace.data_ptr(), nbytes))
@@ -729,6 +747,8 @@ def gated_norm(y, z, weight, ngroups: int = 1, gate_first: bool = True, eps: flo
     channels, v / sqrt(mean(v^2) + eps) * weight for v = y silu(z) (gate_first), or the norm of y times
     silu(z).  y [..., D] in z's dtype or fp32 (as ssd_prefill writes it; heads are flattened by the caller); z
     fp32 or bf16, its rows may be slices of a projection's; weight [D] fp32.  Returns out in z's dtype."""
+    if stream is not None:
+        return _on(stream, z, gated_norm, y, z, weight, ngroups, gate_first, eps, out)
     dev = _cuda(z, "z")
     if y.dtype not in _DTYPES:
         raise ValueError(f"unsupported y dtype {y.dtype}")
@@ -742,7 +762,7 @@ def gated_norm(y, z, weight, ngroups: int = 1, gate_first: bool = True, eps: flo
     else:
         _ok(out, "out", shape, z.dtype, dev)
     dims = NormDims(rows, D, int(ngroups), gate, D)
-    _call(lib.ssd_gated_norm, dev, stream,
+    _call(lib.ssd_gated_norm, dev,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
            weight.data_ptr(), eps, out.data_ptr()))
     return out
@@ -752,6 +772,9 @@ def gated_norm_backward(dout, y, z, weight, ngroups: int = 1, gate_first: bool =
                         dz=None, dweight=None, workspace=None, stream=None):
     """ssd_gated_norm_backward: gradients of gated_norm from dout (z's dtype).  Returns (dy, dz, dweight); a
     dz given by the caller may be a slice of the projection's gradient."""
+    if stream is not None:
+        return _on(stream, z, gated_norm_backward, dout, y, z, weight, ngroups, gate_first, eps, dy, dz,
+                   dweight, workspace)
     dev = _cuda(z, "z")
     if y.dtype not in _DTYPES:
         raise ValueError(f"unsupported y dtype {y.dtype}")
@@ -770,7 +793,7 @@ def gated_norm_backward(dout, y, z, weight, ngroups: int = 1, gate_first: bool =
     _ok_f32((("weight", weight), ("dweight", dweight)), (D,), dev)
     dims = NormDims(rows, D, int(ngroups), gate, dgate)
     workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
-    _call(lib.ssd_gated_norm_backward, dev, stream,
+    _call(lib.ssd_gated_norm_backward, dev,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
            weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(),
            workspace.data_ptr(), nbytes))

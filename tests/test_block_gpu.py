@@ -412,9 +412,33 @@ def test_explicit_stream_argument(ssd):
     want = ssd.glr_prefill(t["x"], t["r"], t["i"], t["A"])[0]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    h = ssd.glr_prefill(t["x"], t["r"], t["i"], t["A"], stream=side)[0]
-    side.synchronize()
-    assert torch.equal(h, want)
+    for stream in (side, side.cuda_stream):
+        h = ssd.glr_prefill(t["x"], t["r"], t["i"], t["A"], stream=stream)[0]
+        side.synchronize()
+        assert torch.equal(h, want)
+
+
+def test_memory_of_a_call_on_another_stream_is_not_reused(ssd):
+    """Workspaces that a call allocates live until its stream has used them: while the side stream is held back, the
+    current one allocates and overwrites blocks of their size."""
+    t = _inputs(20, b=2, L=600)
+    dout, s = t["dh"], t["x"].float()
+    calls = [lambda **k: ssd.glr_backward(t["x"], t["r"], t["i"], t["A"], t["x"], t["dh"], t["h0"], **k),
+             lambda **k: ssd.residual_norm_backward(dout, s, t["w"], x=t["x"], scale=t["sc"], **k),
+             lambda **k: ssd.gated_norm_backward(dout, s, t["x"], t["w"], **k)]
+    want = [c() for c in calls]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, ref in zip(calls, want):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        got = call(stream=side)
+        for n in (1 << 12, 1 << 16, 600 * 2 * 272 * 2, 1 << 20, 4 << 20):
+            for _ in range(4):
+                torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
 def test_offsets_beyond_32_bits(ssd):
