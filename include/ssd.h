@@ -432,8 +432,9 @@ SSD_API ssd_status ssd_glr_backward(const ssd_glr_dims *dims, ssd_dtype dtype, c
  * output is rounded once, to nearest even.  Arrays are row-major and contiguous except the
  * gate z and its gradient, whose rows are gate_stride and dgate_stride elements apart (a
  * slice of the block's input projection).  Arrays need only the alignment of their
- * elements; 16-byte aligned arrays whose rows and groups are multiples of 16 bytes take the
- * wide-load path.  weight, scale, dweight and dscale are fp32 [dim].
+ * elements; 16-byte aligned arrays (32 for fp32 ones beside bf16) whose rows and groups are
+ * multiples of 16 bytes (32) take the wide-load path.  weight, scale, dweight and dscale are
+ * fp32 [dim].
  */
 typedef struct {
   int64_t rows;         /* >= 0                                                               */

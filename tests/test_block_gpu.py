@@ -407,6 +407,40 @@ def test_outputs_not_wanted(ssd):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("shift", [4, 8, 2, 1])
+def test_norms_at_every_alignment(ssd, shift):
+    """Arrays and workspaces `shift` fp32 (4: 16 bytes, but not 32) from an aligned address give the aligned ones' bits
+    where the same path runs, and the oracle's values anyway."""
+    gen, rows, D = _gen(21), 70, 512
+
+    def moved(t):
+        base = torch.empty(t.numel() + shift, dtype=t.dtype, device="cuda")[shift:]
+        return base.view(t.shape).copy_(t)
+
+    x, dout = _rand(gen, rows, D, dtype=BF), _rand(gen, rows, D, dtype=BF)
+    y, res, w, sc = _rand(gen, rows, D), _rand(gen, rows, D), 1 + _rand(gen, D, std=0.1), _rand(gen, D)
+    nbytes = 1 << 22
+    ws = torch.empty(nbytes + 16, dtype=torch.uint8, device="cuda")[16:]
+    m = [moved(t) for t in (x, dout, y, res, w, sc)]
+    for a in ((x, dout, y, res, w, sc), m, (x, dout, moved(y), res, moved(w), moved(sc))):
+        X, U, Y, R, Wt, S = a
+        so = moved(R)
+        out, s = ssd.residual_norm(X, Wt, residual=R, scale=S, residual_out=so, eps=EPS)
+        ro, rsum, bo, bs = block.residual_norm(_np(x), _np(sc), _np(res), _np(w), EPS)
+        check(out, ro, bo, "out")
+        check(s, rsum, bs, "residual_out")
+        got = ssd.residual_norm_backward(U, s, Wt, x=X, scale=S, dresidual_out=Y, eps=EPS, dresidual=moved(Y), workspace=ws)
+        want, tol = block.residual_norm_backward(_np(x), _np(sc), _np(s), _np(w), EPS, _np(dout), _np(y))
+        for g, name in zip(got, ("dx", "dres", "dw", "dscale")):
+            check(g, want[name], tol[name], name)
+        got = ssd.gated_norm_backward(U, Y, X, Wt, ngroups=2, eps=EPS, dy=moved(Y), dz=moved(X), workspace=ws)
+        want, tol = block.gated_norm_backward(_np(y), _np(x), _np(w), 2, True, EPS, _np(dout))
+        for g, name in zip(got, ("dy", "dz", "dw")):
+            check(g, want[name], tol[name], name)
+        check(ssd.gated_norm(Y, X, Wt, ngroups=2, eps=EPS, out=moved(X)),
+              *block.gated_norm(_np(y), _np(x), _np(w), 2, True, EPS), "gated")
+
+
 def test_explicit_stream_argument(ssd):
     t = _inputs(15, b=1, L=200)
     want = ssd.glr_prefill(t["x"], t["r"], t["i"], t["A"])[0]
