@@ -81,12 +81,20 @@ struct Runs {
   using Piece = std::conditional_t<(VEC > 1), uint4, T>;
   Piece q[NV][kPieces];
 
-  // from memory: run k at p + at[k]
+  // from memory: run k at p + at[k]; kSectors: a run of 8 fp32 at once
+  template <bool kSectors = false>
   __device__ __forceinline__ void load(const T *p, const int (&at)[NV]) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
+      if constexpr (kSectors && VEC == 8 && sizeof(T) == 4) {
+        ulonglong2 a, b;
+        asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(a.x), "=l"(a.y), "=l"(b.x), "=l"(b.y) : "l"(p + at[k]));
+        q[k][0] = *reinterpret_cast<uint4 *>(&a);
+        q[k][1] = *reinterpret_cast<uint4 *>(&b);
+      } else {
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) q[k][j] = reinterpret_cast<const Piece *>(p + at[k])[j];
+        for (int j = 0; j < kPieces; ++j) q[k][j] = reinterpret_cast<const Piece *>(p + at[k])[j];
+      }
   }
   // from the thread's pieces in shared memory, `pitch` apart; those of a run begin `run` pieces after the last one's
   __device__ __forceinline__ void load_pieces(const uint4 *from, int run, int pitch) {
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(row_threads(NV *VEC))
   Runs<TX, VEC, NV> rx;
   Runs<TR, VEC, NV> rw;
   rx.load(x + row * (M == kResidual ? d.D : d.gate) + c0, at);
-  if (M != kResidual || wide != nullptr) rw.load(wide + row * d.D + c0, at);
+  if (M != kResidual || wide != nullptr) rw.template load<true>(wide + row * d.D + c0, at);
   f2 v[E], gate[M == kNormFirst ? E : 1];
   if (M == kResidual) {
     if (scale != nullptr) {
