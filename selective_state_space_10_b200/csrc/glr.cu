@@ -129,7 +129,7 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
 // them through distributed shared memory.
 // Warps, tokens a warp and CTAs an SM of each scan.  Long runs of tokens amortise a tile's exchange, small CTAs keep the
 // SMs evenly loaded (2.7B-shaped bf16 prefill: 4 x 16 47.8 us, 4 x 12 54.0, 4 x 8 54.3, 2 x 16 57.2, 8 x 16 66.5 us;
-// long-context bf16 gradient: 4 x 12 381 us, 4 x 8 408, 2 x 12 437, 4 x 4 490, 8 x 8 509 us).  fp32 tiles are twice
+// long-context bf16 gradient: 4 x 12 381 us, 4 x 8 408, 2 x 12 437, 4 x 4 490, 8 x 8 509 us, before the last step).  fp32 tiles are twice
 // the bytes; the prefill runs the same with any of these shapes, and the gradient's short runs leave room for four CTAs
 // (b = 4, L = 4096, D = 5120: 4 x 4 442 us, 4 x 8 507 us; b = 1, L = 16384, D = 1536: 182 and 150 us).
 template <typename T>
