@@ -16,7 +16,7 @@ using ssd::check_ptr;
 using ssd::cuda_status;
 using ssd::Dims;
 
-constexpr int kVersion = 100;  // 0.1.0
+constexpr int kVersion = 200;  // 0.2.0
 constexpr size_t kAlign = 256;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }

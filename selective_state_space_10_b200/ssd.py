@@ -6,6 +6,7 @@ and forwards raw device pointers and the current CUDA stream through ctypes.  Im
 it loads libssd.so and raises if the library has not been built: there is no fallback.
 """
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -558,6 +559,16 @@ def _new(like: torch.Tensor, shape, dtype) -> torch.Tensor:
     return like.new_empty(shape, dtype=dtype)
 
 
+@functools.lru_cache(maxsize=256)  # sizes depend on these numbers alone
+def _glr_workspace(b: int, L: int, D: int, dtype: int) -> int:
+    return lib.ssd_glr_backward_workspace_size(ctypes.byref(GlrDims(b, L, D, D, D)), dtype)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(rows: int, D: int) -> int:
+    return lib.ssd_norm_backward_workspace_size(ctypes.byref(NormDims(rows, D, 1, D, D)))
+
+
 def _workspace(workspace, need: int, like: torch.Tensor):
     if workspace is None:
         return like.new_empty(need, dtype=torch.uint8), need
@@ -634,19 +645,19 @@ def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=No
     row = _same_stride(_XRI, x, r, i, shape, x.dtype, dev)
     _ok(h, "h", shape, x.dtype, dev)
     _ok(dh, "dh", shape, x.dtype, dev)
-    dx = torch.empty_like(h) if dx is None else dx
-    dr = torch.empty_like(h) if dr is None else dr
-    di = torch.empty_like(h) if di is None else di
-    grad = _same_stride(_GRADS, dx, dr, di, shape, x.dtype, dev)
-    dA = torch.empty_like(A) if dA is None else dA
     _ok_f32((("A", A), ("dA", dA)), (D,), dev)
-    if dinitial_state is None:
-        dinitial_state = _new(A if dfinal_state is None else dfinal_state, (b, D), torch.float32)
     _ok_f32((("initial_state", initial_state), ("dfinal_state", dfinal_state), ("dinitial_state", dinitial_state)),
             (b, D), dev)
+    if dx is None and dr is None and di is None:
+        dx, dr, di, grad = torch.empty_like(h), torch.empty_like(h), torch.empty_like(h), D
+    else:
+        dx, dr, di = (torch.empty_like(h) if t is None else t for t in (dx, dr, di))
+        grad = _same_stride(_GRADS, dx, dr, di, shape, x.dtype, dev)
+    dA = torch.empty_like(A) if dA is None else dA
+    if dinitial_state is None:
+        dinitial_state = _new(A if dfinal_state is None else dfinal_state, (b, D), torch.float32)
     dims = GlrDims(b, L, D, row, grad)
-    need = lib.ssd_glr_backward_workspace_size(ctypes.byref(dims), _DTYPES[x.dtype])
-    workspace, nbytes = _workspace(workspace, need, A)
+    workspace, nbytes = _workspace(workspace, _glr_workspace(b, L, D, _DTYPES[x.dtype]), A)
     _call(lib.ssd_glr_backward, dev,
           (ctypes.byref(dims), _DTYPES[x.dtype], x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
            _address(initial_state), h.data_ptr(), dh.data_ptr(), _address(dfinal_state), dx.data_ptr(),
@@ -730,10 +741,10 @@ def residual_norm_backward(dout, s, weight, x=None, scale=None, dresidual_out=No
         dresidual = torch.empty_like(s)
     else:
         _ok(dresidual, "dresidual", shape, s.dtype, dev)
-    dweight = torch.empty_like(weight) if dweight is None else dweight
     _ok_f32((("weight", weight), ("scale", scale), ("dweight", dweight), ("dscale", dscale)), (D,), dev)
+    dweight = torch.empty_like(weight) if dweight is None else dweight
     dims = NormDims(rows, D, 1, D, D)
-    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
+    workspace, nbytes = _workspace(workspace, _norm_workspace(rows, D), weight)
     _call(lib.ssd_residual_norm_backward, dev,
           (ctypes.byref(dims), _DTYPES[dout.dtype], _DTYPES[s.dtype], _address(x if scale is not None else None),
            _address(scale), s.data_ptr(), weight.data_ptr(), eps, dout.data_ptr(), _address(dresidual_out),
@@ -787,12 +798,14 @@ def gated_norm_backward(dout, y, z, weight, ngroups: int = 1, gate_first: bool =
         dy = torch.empty_like(y)
     else:
         _ok(dy, "dy", shape, y.dtype, dev)
-    dz = torch.empty_like(dout) if dz is None else dz
-    dgate = _row_stride(dz, "dz", shape, z.dtype, dev)
-    dweight = torch.empty_like(weight) if dweight is None else dweight
+    if dz is None:
+        dz, dgate = torch.empty_like(dout), D
+    else:
+        dgate = _row_stride(dz, "dz", shape, z.dtype, dev)
     _ok_f32((("weight", weight), ("dweight", dweight)), (D,), dev)
+    dweight = torch.empty_like(weight) if dweight is None else dweight
     dims = NormDims(rows, D, int(ngroups), gate, dgate)
-    workspace, nbytes = _workspace(workspace, lib.ssd_norm_backward_workspace_size(ctypes.byref(dims)), weight)
+    workspace, nbytes = _workspace(workspace, _norm_workspace(rows, D), weight)
     _call(lib.ssd_gated_norm_backward, dev,
           (ctypes.byref(dims), _DTYPES[z.dtype], _DTYPES[y.dtype], int(bool(gate_first)), y.data_ptr(), z.data_ptr(),
            weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(), dweight.data_ptr(),

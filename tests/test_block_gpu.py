@@ -575,6 +575,43 @@ def test_a_trained_block(ssd):
         assert err < 1e-4, (name, float(err))
 
 
+def test_calls_back_to_back_wait_for_one_another(ssd):
+    """Each kernel may be launched before the last one ends, and reads nothing of it before that: a chain through both
+    mixers and all norms, each call on the outputs of the one before and outputs reused from turn to turn, gives the
+    bits of the same chain with the GPU idle between calls."""
+    from selective_state_space_10_b200 import inputs
+    from helpers import to_device
+    b, L, H, P = 1, 512, 8, 64
+    D = H * P
+    seq = to_device(inputs.sequence(b, L, H, P, 128, 1, "bf16", seed=7))
+    gen = _gen(22)
+    x0, z, w, sc = _rand(gen, b, L, D, dtype=BF), _rand(gen, b, L, D, dtype=BF), 1 + _rand(gen, D, std=0.1), _rand(gen, D)
+    A = _decays(gen, D)
+
+    def chain(idle):
+        x, res, state = x0.clone(), torch.zeros(b, L, D, device="cuda"), torch.zeros(b, D, device="cuda")
+        n, g, h = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        sync = torch.cuda.synchronize if idle else lambda: None
+        kept = []
+        for turn in range(12):
+            ssd.residual_norm(x, w, residual=res, scale=sc, residual_out=res, out=n); sync()
+            ssd.glr_prefill(n, z, n, A, initial_state=state, h=h, final_state=state); sync()
+            y, _ = ssd.prefill(h.view(b, L, H, P), seq["dt"], seq["A"], seq["B"], seq["C"], seq["D"], chunk=256); sync()
+            ssd.gated_norm(y.view(b, L, D), z, w, ngroups=4, out=g); sync()
+            ssd.glr_decode_step(state, g[:, 0].contiguous(), z[:, 0].contiguous(), n[:, 0].contiguous(), A); sync()
+            grads = ssd.glr_backward(n, z, n, A, h, g, state); sync()
+            dy, dz, dw = ssd.gated_norm_backward(grads[0], y.view(b, L, D), z, w, ngroups=4); sync()
+            out = ssd.residual_norm_backward(dz, res, w, x=x, scale=sc, dresidual_out=dy); sync()
+            x.copy_(g); sync()
+            kept += [t.clone() for t in (n, h, g, state, *grads, dy, dz, dw, *out)]; sync()
+        torch.cuda.synchronize()
+        return kept
+
+    apart = chain(True)
+    for _ in range(3):
+        assert all(torch.equal(a, c) for a, c in zip(chain(False), apart))
+
+
 def test_binding_refusals_on_the_gpu(ssd):
     t = _inputs(18, L=8)
     with pytest.raises(ValueError, match="dtype"):
