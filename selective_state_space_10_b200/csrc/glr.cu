@@ -378,7 +378,7 @@ __device__ __forceinline__ Place place(int64_t D, int blocks) {
 }
 
 // The forward scan.  2.7B-shaped bf16 layer (b = 1, L = 4096, D = 5120): 47.4 us for 168 MB, 3.5 TB/s, 54 % of the
-// measured copy bandwidth; fp32 57.5 us, 5.8 TB/s.  The bf16 scan has twice the elements a byte: 35 warp instructions and
+// measured copy bandwidth; fp32 55.7 us, 6.0 TB/s.  The bf16 scan has twice the elements a byte: 35 warp instructions and
 // 4 special functions for each, issue slots 50 % and special-function units 46 % busy with the 10 warps an SM that 160
 // registers leave; what remains is their latency.  Forming the next tile's gates while a tile's exchange is under way
 // (a second set of registers, 8 warps an SM) measured 64 us.
@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
     Link all = {a[0], v[0]};
 #pragma unroll
     for (int j = 1; j < kT; ++j) all = then(all, {a[j], v[j]});
-    load(par, left - 2 * step);
     ex.publish(all);
+    load(par, left - 2 * step);  // while the ranks' messages travel
     s = ex.collect();
     if (left >= kT) {
 #pragma unroll
