@@ -654,7 +654,13 @@ cudaError_t norm(const TX *x, const float *scale, const TR *wide, const float *w
   return cudaGetLastError();
 }
 
-// Runs the register kernel and sets `parts`; false: rows too long for it.
+// Most dynamic shared memory of a CTA: 227 KB but for the kernel's own arrays.
+constexpr int kMaxSmem = 227 * 1024 - 512;
+
+// Runs the register kernel and sets `parts`; false: rows too long for it, or for one stage of its ring beside the weights
+// in the shared memory of a CTA (residual norm with 16 channels a thread: from 9220 fp32 channels with a scale, 11268
+// without, 11272 bf16 ones beside fp32 with a scale).  The kernel for long rows takes those at about half the rate: 2048
+// rows of bf16 beside fp32 with a scale, 11264 channels here 182 us, 12288 there 396 us.
 template <Mode M, typename TX, typename TR, int VEC, int NV>
 bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const float *w, float eps, const TX *dout,
                         const TR *dwide, TX *dx, TR *dwide_out, float *pw, float *ps, const NormDims &d, int &parts,
@@ -664,12 +670,13 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
   if (tpr == 0) return false;
   const int subs = std::max(1, 256 / tpr), threads = subs * tpr;
   const int resident = std::max(1, kRowThreads / threads);
-  parts = (int)std::max<int64_t>(1, std::min<int64_t>({(d.rows + subs - 1) / subs, 148 * resident / d.G, parts}));
   using P = Pieces<M, TX, TR, VEC>;
   const int stage = VEC > 1 ? threads * NV * P::all * 16 : 0;
   const int fixed = VEC > 1 ? threads * NV * P::kF * 16 * (M == kResidual && scale != nullptr ? 2 : 1) : 0;
   const int stages = VEC > 1 ? std::max(1, std::min(4, (kRingBytes / resident - fixed) / stage)) : 1;
   const size_t smem = std::max((size_t)stages * stage + fixed, (size_t)threads * VEC * NV * 4);
+  if (smem > kMaxSmem) return false;
+  parts = (int)std::max<int64_t>(1, std::min<int64_t>({(d.rows + subs - 1) / subs, 148 * resident / d.G, parts}));
   auto *f = k_norm_backward_rows<M, TX, TR, VEC, NV>;
   err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return true;
