@@ -16,7 +16,13 @@ inline bool check_ptr(const void *p, int64_t elems, size_t align) {
   return p != nullptr && aligned(p, align);
 }
 
-inline ssd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
+// The status of a call's last runtime call.  The runtime also keeps an error for whoever asks it next
+// (cudaGetLastError), which would be the thread's next call here: it is cleared, so that each call answers for itself.
+inline ssd_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return SSD_OK;
+  cudaGetLastError();
+  return SSD_ERR_CUDA;
+}
 
 ssd_status prefill_into_workspace(const ssd_dims *dims, ssd_dtype dtype, const void *x, const float *dt,
                                   const float *A, const void *B, const void *C, const float *D, int chunk,

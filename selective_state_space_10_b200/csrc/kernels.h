@@ -9,10 +9,9 @@
 
 namespace ssd {
 
-// Launches f as a programmatic dependent of what the stream ran before: its CTAs take their places as the last ones of
-// that kernel leave theirs, and f itself waits (grid_dep_wait, before it touches memory) until that kernel is complete.
+// Launches f; the status is this launch's own.
 template <typename... P, typename... V>
-cudaError_t launch_dependent(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, V... v) {
+cudaError_t launch(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool dependent, V... v) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -22,8 +21,15 @@ cudaError_t launch_dependent(void (*f)(P...), dim3 grid, int threads, size_t sme
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = dependent ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, f, P(v)...);
+}
+
+// The same as a programmatic dependent of what the stream ran before: its CTAs take their places as the last ones of
+// that kernel leave theirs, and f itself waits (grid_dep_wait, before it touches memory) until that kernel is complete.
+template <typename... P, typename... V>
+cudaError_t launch_dependent(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, V... v) {
+  return launch(f, grid, threads, smem, st, true, v...);
 }
 
 // prefill_simt.cu

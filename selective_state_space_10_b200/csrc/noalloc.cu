@@ -62,6 +62,11 @@ unsigned long long current_context_id() {
   return id;
 }
 
+ssd_status look_up(void **p) {
+  const cudaError_t e = cudaGetSymbolAddress(p, g_noalloc_scratch);
+  return e == cudaSuccess && *p == nullptr ? SSD_ERR_CUDA : ssd::cuda_status(e);
+}
+
 // Device address of the scratch array in the current context (looked up on first use).
 ssd_status scratch_in_current_context(void **out) {
   std::lock_guard<std::mutex> lock(g_table.mu);
@@ -76,7 +81,8 @@ ssd_status scratch_in_current_context(void **out) {
   if (id == 0) {
     // No context bound to this thread yet: the runtime binds its primary context of the
     // current device on its first call, which this look-up is.
-    if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr) return SSD_ERR_CUDA;
+    const ssd_status s = look_up(&p);
+    if (s != SSD_OK) return s;
     if ((id = current_context_id()) == 0) return SSD_ERR_CUDA;
   }
   for (int i = 0; i < g_table.used; ++i)
@@ -84,7 +90,10 @@ ssd_status scratch_in_current_context(void **out) {
       *out = g_table.ptr[i];
       return SSD_OK;
     }
-  if (p == nullptr && (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr)) return SSD_ERR_CUDA;
+  if (p == nullptr) {
+    const ssd_status s = look_up(&p);
+    if (s != SSD_OK) return s;
+  }
   const int slot = g_table.used < ScratchTable::kEntries ? g_table.used++ : (g_table.next++ % ScratchTable::kEntries);
   g_table.id[slot] = id;
   g_table.ptr[slot] = p;

@@ -650,8 +650,8 @@ cudaError_t norm(const TX *x, const float *scale, const TR *wide, const float *w
   if (vec ? norm_rows<M, TX, TR, VEC>(x, scale, wide, w, eps, wide_out, out, d, err, st)
           : norm_rows<M, TX, TR, 1>(x, scale, wide, w, eps, wide_out, out, d, err, st))
     return err;
-  k_norm<M, TX, TR><<<(unsigned)(d.rows * d.G), kThreads, 0, st>>>(x, scale, wide, w, eps, wide_out, out, d);
-  return cudaGetLastError();
+  return launch(k_norm<M, TX, TR>, dim3((unsigned)(d.rows * d.G)), kThreads, 0, st, false, x, scale, wide, w, eps, wide_out,
+                out, d);
 }
 
 // Most dynamic shared memory of a CTA: 227 KB but for the kernel's own arrays.
@@ -716,10 +716,9 @@ cudaError_t norm_backward(const TX *x, const float *scale, const TR *wide, const
                 : rows(std::integral_constant<int, 8 / VEC>{}, std::integral_constant<int, VEC>{});
   else
     done = rows(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-  if (!done) {
-    k_norm_backward<M, TX, TR><<<parts, kThreads, 0, st>>>(x, scale, wide, w, eps, dout, dwide, dx, dwide_out, pw, ps, d);
-    e = cudaGetLastError();
-  }
+  if (!done)
+    e = launch(k_norm_backward<M, TX, TR>, dim3((unsigned)parts), kThreads, 0, st, false, x, scale, wide, w, eps, dout, dwide,
+               dx, dwide_out, pw, ps, d);
   if (e != cudaSuccess || (dw == nullptr && ds == nullptr)) return e;
   return launch_row_sums(pw, ps, dw, ds, d.D, parts, st);
 }

@@ -4,6 +4,7 @@
 // sets the workspace's error word exactly as a prefill kernel would, and the kernel
 // returns; the host then reads the word back with ssd_prefill_device_status.  No trap,
 // no fault, no endless loop: the context stays usable.
+#include "api_internal.h"
 #include "common.cuh"
 #include "sm100.cuh"
 #include "ssd.h"
@@ -34,7 +35,8 @@ extern "C" SSD_API ssd_status ssd_wait_selftest(void *workspace, size_t workspac
     return SSD_ERR_INVALID_ARG;
   if (limit_ns == 0 || limit_ns > 100000000ull) return SSD_ERR_INVALID_ARG;  // at most 100 ms
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(int), st) != cudaSuccess) return SSD_ERR_CUDA;
+  const ssd_status s = ssd::cuda_status(cudaMemsetAsync(workspace, 0, sizeof(int), st));
+  if (s != SSD_OK) return s;
   ssd::k_wait_selftest<<<1, 64, 0, st>>>(static_cast<int *>(workspace), limit_ns, expire ? 1 : 0);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  return ssd::cuda_status(cudaGetLastError());
 }

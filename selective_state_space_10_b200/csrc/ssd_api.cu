@@ -201,7 +201,7 @@ static ssd_status prefill_impl(const ssd_dims *dims, ssd_dtype dtype, const void
         reinterpret_cast<float *>(ws + pl.states_off),
         reinterpret_cast<float *>(ws + pl.cdecay_off), reinterpret_cast<__nv_bfloat16 *>(ws + pl.hprev_off),
         reinterpret_cast<int *>(ws), d, chunk, pl.nc, st, ev));
-  if (cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return SSD_ERR_CUDA;
+  if ((s = cuda_status(cudaMemsetAsync(ws, 0, sizeof(int), st))) != SSD_OK) return s;
   if (dtype == SSD_F32)
     return run_prefill<float>(d, chunk, pl, static_cast<const float *>(x), dt, A, static_cast<const float *>(B),
                               static_cast<const float *>(C), D, init, y, final_state, cstates, ws, st, ev);
@@ -329,8 +329,9 @@ ssd_status ssd_prefill_device_status(const void *workspace, size_t workspace_byt
   if (workspace == nullptr || workspace_bytes < sizeof(int) || !aligned(workspace, 16)) return SSD_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int word = 0;
-  if (cudaMemcpyAsync(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess) return SSD_ERR_CUDA;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return SSD_ERR_CUDA;
+  cudaError_t e = cudaMemcpyAsync(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_status(e);
   return word == 0 ? SSD_OK : SSD_ERR_TIMEOUT;
 }
 

@@ -1,5 +1,8 @@
 """GPU tests of the gated linear recurrence and the norms at the limits of what their calls allow: the widest rows, calls
 from several host threads, calls after a failed one, the strongest decays and nearly shut gates."""
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -59,3 +62,52 @@ def test_gated_gradient_of_wide_rows(ssd, D, G, types, gate_first):
     want, tol = block.gated_norm_backward(_np(y), _np(z), _np(w), G, gate_first, EPS, _np(dout))
     for g, name in zip(got, ("dy", "dz", "dw")):
         check(g, want[name], tol[name], name)
+
+
+def test_a_failed_call_is_reported_once():
+    """A launch that the runtime refuses is reported by the call that made it, and the next good call in the thread
+    answers for itself.  The refused launches go to the legacy stream while this thread captures another, blocking
+    stream, which the runtime forbids; nothing of them reaches the GPU."""
+    code = """
+import torch
+from cuda.bindings import runtime as rt
+from selective_state_space_10_b200 import ssd
+f = lambda *s: torch.randn(*s, device='cuda')
+y, w, A = f(9, 256), f(256), -f(256).abs()
+h, st = f(9, 256), f(2, 4, 64, 16)
+x4, B4, dt, a4, o4 = f(2, 4, 64), f(2, 1, 16), f(2, 4).abs(), -f(4).abs(), torch.empty(2, 4, 64, device='cuda')
+out = torch.empty_like(y)
+nd, gd, sd = ssd.NormDims(9, 256, 1, 256, 256), ssd.GlrDims(1, 9, 256, 256, 256), ssd.Dims(2, 1, 4, 64, 16, 1)
+wide = f(3, 40000)
+ww, wo, wd = f(40000), torch.empty_like(wide), ssd.NormDims(3, 40000, 1, 40000, 40000)
+last = torch.empty(1, 256, device='cuda')
+p = lambda t: t.data_ptr()
+fails = dict(
+    norm=lambda s: ssd.lib.ssd_gated_norm(nd, 0, 0, 1, p(y), p(h), p(w), 1e-5, p(out), s),
+    long_norm=lambda s: ssd.lib.ssd_gated_norm(wd, 0, 0, 1, p(wide), p(wide), p(ww), 1e-5, p(wo), s),
+    scan=lambda s: ssd.lib.ssd_glr_prefill(gd, 0, p(y), p(h), p(y), p(A), None, p(out), p(last), s),
+    step=lambda s: ssd.lib.ssd_glr_decode_step(ssd.GlrDims(1, 1, 256, 256, 256), 0, p(last), p(y), p(h), p(y), p(A), p(out), s))
+good = dict(
+    decode=lambda s: ssd.lib.ssd_decode_step(sd, 0, p(st), p(x4), p(dt), p(a4), p(B4), p(B4), p(a4), p(o4), s),
+    long_norm=fails['long_norm'])
+for fn in list(fails.values()) + list(good.values()):
+    assert fn(torch.cuda.current_stream().cuda_stream) == ssd.OK
+torch.cuda.synchronize()
+def do(r):
+    assert r[0] == rt.cudaError_t.cudaSuccess, r
+    return r[1] if len(r) == 2 else None
+for name, bad in fails.items():
+    for after, fn in good.items():
+        s = do(rt.cudaStreamCreate())
+        do(rt.cudaStreamBeginCapture(s, rt.cudaStreamCaptureMode.cudaStreamCaptureModeGlobal))
+        first = bad(None)
+        rt.cudaStreamEndCapture(s)  # the refused launch has invalidated it
+        rt.cudaGetLastError()
+        assert first == ssd.ERR_CUDA, (name, first)
+        assert fn(torch.cuda.current_stream().cuda_stream) == ssd.OK, (name, after)
+        torch.cuda.synchronize()
+        do(rt.cudaStreamDestroy(s))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
