@@ -613,14 +613,14 @@ int copy_width(std::initializer_list<const void *> arrays, std::initializer_list
 }
 bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// The launch of a scan kernel: `ranks` CTAs share a sequence and are a cluster.
-template <typename F>
-cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], F *f, int64_t ctas, int ranks, int warps, size_t smem,
-                   cudaStream_t st) {
+// The launch of a scan kernel: `ranks` CTAs share a sequence and are a cluster.  The kernel's limits are set to the same
+// values in every call: another thread's call with a size of its own may come between this and the launch.
+template <typename T, int N, int kW, int kT, typename F>
+cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], F *f, int64_t ctas, int ranks, cudaStream_t st) {
   cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3((unsigned)(ctas * ranks));
-  cfg.blockDim = dim3(warps * 32);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(kW * 32);
+  cfg.dynamicSmemBytes = scan_smem<T, N, kW, kT>(ranks);
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -628,7 +628,8 @@ cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], F *f, 
   at[1].val.clusterDim = {(unsigned)ranks, 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = ranks > 1 ? 2 : 1;
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)scan_smem<T, N, kW, kT>(kMaxRanks));
   if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
@@ -647,7 +648,7 @@ cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) 
     if (fit < 0) {
       cudaLaunchConfig_t cfg;
       cudaLaunchAttribute at[2];
-      cudaError_t e = set_up(cfg, at, many, 1, ranks, kW, scan_smem<T, N, kW, kT>(ranks), nullptr);
+      cudaError_t e = set_up<T, N, kW, kT>(cfg, at, many, 1, ranks, nullptr);
       if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, many, &cfg);
       if (e != cudaSuccess) return e;
       held[ranks].store(fit + 1, std::memory_order_relaxed);
@@ -662,7 +663,7 @@ cudaError_t launch_scan(void (*one)(P...), void (*many)(P...), int64_t ctas, int
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute at[2];
   auto *f = ranks > 1 ? many : one;
-  cudaError_t e = set_up(cfg, at, f, ctas, ranks, kW, scan_smem<T, N, kW, kT>(ranks), st);
+  cudaError_t e = set_up<T, N, kW, kT>(cfg, at, f, ctas, ranks, st);
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, f, v...);
 }
 

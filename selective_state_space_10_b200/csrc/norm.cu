@@ -678,7 +678,8 @@ bool norm_backward_rows(const TX *x, const float *scale, const TR *wide, const f
   if (smem > kMaxSmem) return false;
   parts = (int)std::max<int64_t>(1, std::min<int64_t>({(d.rows + subs - 1) / subs, 148 * resident / d.G, parts}));
   auto *f = k_norm_backward_rows<M, TX, TR, VEC, NV>;
-  err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same limit in every call: another thread's call with a size of its own may come between this and the launch
+  err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (err != cudaSuccess) return true;
   err = launch_dependent(f, dim3((unsigned)(parts * d.G)), threads, smem, st, x, scale, wide, w, eps, dout, dwide, dx,
                          dwide_out, pw, ps, d, tpr, (int)W, parts, stages);

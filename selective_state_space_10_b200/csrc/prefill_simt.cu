@@ -306,8 +306,9 @@ cudaError_t launch_chunk_scan_simt(const T *x, const float *dt, const T *B, cons
                                    const float *cum, const float *hprev, float *y, const Dims &d, int Q,
                                    int nc, cudaStream_t st) {
   const size_t smem = chunk_scan_simt_smem_bytes(d.N);
+  // the largest state's in every call: another thread's call may come between this and the launch
   cudaError_t e = cudaFuncSetAttribute(k_chunk_scan_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)chunk_scan_simt_smem_bytes(256));
   if (e != cudaSuccess) return e;
   const dim3 grid(d.b * d.H * nc, ((Q + 63) / 64) * ((d.P + 63) / 64));
   k_chunk_scan_simt<T><<<grid, 256, smem, st>>>(x, dt, B, C, D, cum, hprev, y, d, Q, nc);

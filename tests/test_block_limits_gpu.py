@@ -1,5 +1,6 @@
 """GPU tests of the gated linear recurrence and the norms at the limits of what their calls allow: the widest rows, calls
 from several host threads, calls after a failed one, the strongest decays and nearly shut gates."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -111,3 +112,43 @@ for name, bad in fails.items():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+class _Job(ctypes.Structure):  # `job` of call_in_threads.c
+    _fields_ = ([("fn", ctypes.c_void_p)] + [(k, ctypes.c_int64) for k in ("scan", "rows", "dim")] +
+                [(k, ctypes.c_void_p) for k in ("input", "weight", "out", "vec", "workspace", "stream")] +
+                [(k, ctypes.c_int64) for k in ("workspace_bytes", "calls", "failed")] + [("thread", ctypes.c_ulong)])
+
+
+def test_host_threads_with_calls_of_different_sizes(ssd, tmp_path):
+    """No call depends on the sizes of another thread's: threads that call the same kernels with little and with much
+    shared memory, all at once, each get what the same call gives alone."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    lib = str(tmp_path / "threads.so")
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-I" + os.path.join(os.path.dirname(here), "include"),
+                    os.path.join(here, "call_in_threads.c"), "-o", lib, "-lpthread"], check=True)
+    run = ctypes.CDLL(lib).call_in_threads
+    sizes = [(0, 9, 512), (0, 9, 5120), (0, 9, 4096), (0, 9, 8192), (1, 9, 64), (1, 900, 64), (1, 100, 64), (1, 2000, 64)]
+    jobs, held = (_Job * len(sizes))(), []
+    for job, (scan, rows, dim) in zip(jobs, sizes):
+        gen = _gen(rows, dim)
+        x, w = _rand(gen, rows, dim), -_rand(gen, dim).abs()
+        out, vec, side = torch.zeros(2, rows, dim, device="cuda"), torch.zeros(dim, device="cuda"), torch.cuda.Stream()
+        need = ssd.lib.ssd_norm_backward_workspace_size(ssd.NormDims(rows, dim, 1, dim, dim))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        if scan:
+            want = [t.clone() for t in ssd.glr_prefill(x[None], x[None], x[None], w)]
+        else:
+            want = [t.clone() for t in ssd.gated_norm_backward(x, x, x, w)]
+        fn = ssd.lib.ssd_glr_prefill if scan else ssd.lib.ssd_gated_norm_backward
+        job.fn, job.scan, job.rows, job.dim = ctypes.cast(fn, ctypes.c_void_p), scan, rows, dim
+        job.input, job.weight, job.out, job.vec = (t.data_ptr() for t in (x, w, out, vec))
+        job.workspace, job.workspace_bytes, job.stream, job.calls = ws.data_ptr(), need, side.cuda_stream, 3000
+        held.append((x, w, ws, side, out, vec, want))
+    torch.cuda.synchronize()
+    assert run(jobs, len(sizes)) == 1
+    torch.cuda.synchronize()
+    assert [j.failed for j in jobs] == [0] * len(sizes)
+    for (scan, rows, dim), (*_, out, vec, want) in zip(sizes, held):
+        got = [out[0][None], vec[None]] if scan else [out[0], out[1], vec]
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (scan, rows, dim)
