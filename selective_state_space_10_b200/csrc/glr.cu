@@ -37,11 +37,11 @@ __device__ __forceinline__ f2 exp_neg_finite(f2 v) {
 }
 
 // a = exp(L) and v = 1 - a for L <= 0, both to full relative precision: L = n ln 2 + f with |f| <= ln 2 / 2,
-// p = exp(f) - 1 by a polynomial (fitted with relative weights and p'(0) = 1; 1.6e-8 off at most, below half a
-// step of fp32), a = 2^n (1 + p), v = (1 - 2^n) - 2^n p.  1 - a^2 = v (1 + a) then loses nothing for decays close
+// p = 1 - exp(f) by a polynomial (fitted with relative weights and p'(0) = -1; 1.6e-8 off at most, below half a
+// step of fp32), a = 2^n (1 - p), v = (1 - 2^n) + 2^n p.  1 - a^2 = v (1 + a) then loses nothing for decays close
 // to 1; an exp(L) rounded near 1 and subtracted would, and its error would be carried through every step of a
-// long memory.  The exponential unit, which the gates already fill, is not used.
-template <bool kSmall>  // kSmall: a small a is wanted to full relative precision too, not only to that of 1
+// long memory.  Nor is a formed as 1 - v, which would leave a small one the absolute precision of 1.  The exponential
+// unit, which the gates already fill, is not used.
 __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
   const float2 s = split(L);
   L = mk(max_nan(s.x, -87.f), max_nan(s.y, -87.f));  // n >= -126
@@ -58,7 +58,7 @@ __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
   const f2 two_n = mk(__int_as_float((__float_as_int(i.x) << 23) + 0x3f800000),
                       __int_as_float((__float_as_int(i.y) << 23) + 0x3f800000));
   v = fma2(two_n, p, fma2(two_n, both(-1.f), both(1.f)));
-  a = kSmall ? two_n * fma2(p, both(-1.f), both(1.f)) : fma2(v, both(-1.f), both(1.f));
+  a = two_n * fma2(p, both(-1.f), both(1.f));
 }
 
 // One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x, as x rest / sqrt(rest (1 + e)^2) with
@@ -66,7 +66,7 @@ __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
 // square overflow) gives 0; where a is exactly 1, rest is kTiny and 1e-19 of x comes in.
 __device__ __forceinline__ void gate(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b) {
   f2 v;
-  decay<false>(A * rcp(exp_neg(r) + both(1.f)), a, v);
+  decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
   const f2 rest = fma2(v, a, v + both(kTiny)), o = exp_neg(i) + both(1.f);
   b = x * rest * rsqrt_approx(o * o * rest);
 }
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     f2 a[kT], v[kT];
 #pragma unroll
     for (int j = kT - 1; j >= 0; --j)
-      decay<true>(Ac * rcp(exp_neg(load2(&in[0][j][2 * p.lane])) + both(1.f)), a[j], v[j]);
+      decay(Ac * rcp(exp_neg(load2(&in[0][j][2 * p.lane])) + both(1.f)), a[j], v[j]);
     if (t < 0) {  // tokens before the first leave c as it is
 #pragma unroll
       for (int j = 0; j < kT; ++j)

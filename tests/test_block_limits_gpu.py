@@ -5,6 +5,7 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -12,6 +13,7 @@ from oracle import block
 from test_block_gpu import BF, EPS, F32, _gen, _np, _rand, check
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
 
 
 @pytest.fixture(scope="module")
@@ -152,3 +154,42 @@ def test_host_threads_with_calls_of_different_sizes(ssd, tmp_path):
     for (scan, rows, dim), (*_, out, vec, want) in zip(sizes, held):
         got = [out[0][None], vec[None]] if scan else [out[0], out[1], vec]
         assert all(torch.equal(a, b) for a, b in zip(got, want)), (scan, rows, dim)
+
+
+def _kept(ssd, L, D, dtype, gen, strong):
+    """Shut input gates (nothing comes in), so that h = a_1 ... a_t h_0 alone: the recurrence gate is shut too (a = 1)
+    but for the tokens `strong`.  A from -0.01 to -20: decays from 0.99 down to 1e-9 a token."""
+    A = -torch.logspace(-2, np.log10(20.0), D).cuda()
+    r = torch.full((1, L, D), -float("inf"))
+    for t in strong:
+        r[0, t] = torch.randn(D, generator=gen) * 1.5
+    r = r.to(dtype).cuda()
+    i, x = torch.full_like(r, -float("inf")), torch.full_like(r, 3.0)
+    h0 = (0.5 + torch.rand(1, D, generator=gen)).cuda()
+    logs = _np(A) * block.sigmoid(_np(r))
+    ref = _np(h0)[:, None] * np.exp(np.cumsum(logs, axis=1))
+    # a token's decay: its sigmoid within 24 U, the product with A, the range reduction's constant and sum within 2 U of
+    # L, all relative to L; the polynomial, 2^n and 1 - p within 4 U of a, and 2 products (into a tile's update, and of
+    # that with the state) within U each.  At a = 1 nothing is rounded.
+    steps = np.where(logs < 0, 26 * U * np.abs(logs) + 6 * U, 0)
+    return (x, r, i, A, h0), ref, np.abs(ref) * np.expm1(np.cumsum(steps, axis=1)) * 1.01
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("L,strong", [(5, (0, 1, 3)), (1, (0,)), (900, (0, 63, 64, 301, 899))])
+def test_a_small_decay_keeps_its_precision(ssd, L, strong, dtype):
+    """What a token forgets to 1e-9 is that, to the precision of fp32: the decay's own, not 1 - a's."""
+    args, ref, bound = _kept(ssd, L, 120, dtype, _gen(L, 41), strong)
+    x, r, i, A, h0 = args
+    h, last = ssd.glr_prefill(x, r, i, A, initial_state=h0)
+    check(h, ref, bound, "h")
+    check(last, ref[:, -1], bound[:, -1], "final state")
+
+
+@pytest.mark.parametrize("D", [120, 119])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_a_small_decay_of_a_step_keeps_its_precision(ssd, D, dtype):
+    (x, r, i, A, state), ref, bound = _kept(ssd, 1, D, dtype, _gen(D, 42), (0,))
+    h = ssd.glr_decode_step(state, x[:, 0], r[:, 0], i[:, 0], A)
+    check(h, ref[:, 0], bound[:, 0], "h")
+    check(state, ref[:, 0], bound[:, 0], "state")
