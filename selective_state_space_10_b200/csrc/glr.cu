@@ -61,14 +61,28 @@ __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
   a = two_n * fma2(p, both(-1.f), both(1.f));
 }
 
-// One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x, as x rest / sqrt(rest (1 + e)^2) with
-// rest = 1 - a^2 and e = exp(-i): one root in place of a root and a reciprocal.  A shut input gate (e and its
-// square overflow) gives 0; where a is exactly 1, rest is kTiny and 1e-19 of x comes in.
-__device__ __forceinline__ void gate(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b) {
+// One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x, with rest = 1 - a^2 and o = 1 + exp(-i) as
+// x rest / sqrt(rest o^2): one root in place of a root and a reciprocal.  kTiny leaves b exactly 0 where a is 1, and
+// changes nothing from rest = 2e-31 on.  Where the root's argument overflows (i below -44) its sum in `args` is no longer
+// finite, and gate_wide has to be taken.
+__device__ __forceinline__ void gate(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b, f2 &args) {
   f2 v;
   decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
-  const f2 rest = fma2(v, a, v + both(kTiny)), o = exp_neg(i) + both(1.f);
-  b = x * rest * rsqrt_approx(o * o * rest);
+  const f2 rest = fma2(v, a, v), o = exp_neg(i) + both(1.f), arg = fma2(o * o, rest, both(kTiny));
+  b = x * (rest * rsqrt_approx(arg));
+  args = args + arg;
+}
+// The same for every i: a sigmoid down to the end of the normal range.  Its fifth special function for every token would
+// take the 2.7B-shaped bf16 prefill to 50.3 us; the sum of the arguments, and this where it says so, 48.0 us.
+__device__ __forceinline__ void gate_wide(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b) {
+  f2 v;
+  decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
+  const f2 rest = fma2(v, a, v);
+  b = x * rcp(exp_neg(i) + both(1.f)) * (rest * rsqrt_approx(rest + both(kTiny)));
+}
+__device__ __forceinline__ bool finite(f2 args) {  // a sum of terms that are not negative
+  const float2 s = split(args);
+  return s.x + s.y < __int_as_float(0x7f800000);
 }
 
 // One step back: c (in: c_{t+1}, out: c_t = a_t g_t), the gradients of x, r and i, and dA's term.
@@ -377,6 +391,29 @@ __device__ __forceinline__ Place place(int64_t D, int blocks) {
   return p;
 }
 
+// The input terms of a warp's tokens once more, by gate_wide (a scan's lane whose gate found a nearly shut input gate).  A
+// loop of one token at a time leaves each term in the lane's own words of the tile, so that it takes no registers beside
+// the decays.
+template <typename T, int kT>
+__device__ __forceinline__ void wide_loop(T (*in)[kT][kCh], int lane, f2 A) {
+#pragma unroll 1
+  for (int j = 0; j < kT; ++j) {
+    T *x = &in[0][j][2 * lane], *r = &in[1][j][2 * lane], *i = &in[2][j][2 * lane];
+    f2 a, b;
+    gate_wide(load2(x), load2(r), load2(i), A, a, b);
+    const float2 s = split(b);
+    *reinterpret_cast<float *>(x) = s.x;
+    *reinterpret_cast<float *>(i) = s.y;
+  }
+}
+template <typename T, int kT>
+__device__ __forceinline__ void wide_terms(T (&in)[3][kT][kCh], int lane, f2 A, f2 (&b)[kT]) {
+  wide_loop<T, kT>(in, lane, A);
+#pragma unroll
+  for (int j = 0; j < kT; ++j)
+    b[j] = mk(*reinterpret_cast<const float *>(&in[0][j][2 * lane]), *reinterpret_cast<const float *>(&in[2][j][2 * lane]));
+}
+
 // The forward scan.  2.7B-shaped bf16 layer (b = 1, L = 4096, D = 5120): 47.4 us for 168 MB, 3.5 TB/s, 54 % of the
 // measured copy bandwidth; fp32 55.7 us, 6.0 TB/s.  The bf16 scan has twice the elements a byte: 35 warp instructions and
 // 4 special functions for each, issue slots 50 % and special-function units 46 % busy with the 10 warps an SM that 160
@@ -417,10 +454,12 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   auto gates = [&](int stage, int64_t rest, f2 (&a)[kT], f2 (&v)[kT]) {
     wait_async<1>();
     __syncwarp();
-    const auto &in = sm.in[p.warp][stage];
+    auto &in = sm.in[p.warp][stage];
+    auto at = [&](int k, int j) { return load2(&in[k][j][2 * p.lane]); };
+    f2 args = both(0.f);
 #pragma unroll
-    for (int j = 0; j < kT; ++j)
-      gate(load2(&in[0][j][2 * p.lane]), load2(&in[1][j][2 * p.lane]), load2(&in[2][j][2 * p.lane]), Ac, a[j], v[j]);
+    for (int j = 0; j < kT; ++j) gate(at(0, j), at(1, j), at(2, j), Ac, a[j], v[j], args);
+    if (!finite(args)) wide_terms(in, p.lane, Ac, v);
     if (rest < kT) {  // the sequence ends within these tokens: the rest leave the state as it is
 #pragma unroll
       for (int j = 0; j < kT; ++j)
@@ -479,8 +518,8 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
     if (c >= d.D) return;
     const float4 xv = load4(x + at), rv = load4(r + at), iv = load4(i + at), Av = load4(A + c), sv = load4(state + s);
     f2 a0, v0, a1, v1;
-    gate(mk(xv.x, xv.y), mk(rv.x, rv.y), mk(iv.x, iv.y), mk(Av.x, Av.y), a0, v0);
-    gate(mk(xv.z, xv.w), mk(rv.z, rv.w), mk(iv.z, iv.w), mk(Av.z, Av.w), a1, v1);
+    gate_wide(mk(xv.x, xv.y), mk(rv.x, rv.y), mk(iv.x, iv.y), mk(Av.x, Av.y), a0, v0);
+    gate_wide(mk(xv.z, xv.w), mk(rv.z, rv.w), mk(iv.z, iv.w), mk(Av.z, Av.w), a1, v1);
     v0 = fma2(a0, mk(sv.x, sv.y), v0);
     v1 = fma2(a1, mk(sv.z, sv.w), v1);
     const float2 lo = split(v0), hi = split(v1);
@@ -493,7 +532,7 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
   } else {
     const int n = (int)max((int64_t)0, min((int64_t)2, d.D - c));
     f2 a, v;
-    gate(load_n(x + at, n), load_n(r + at, n), load_n(i + at, n), load_n(A + c, n), a, v);
+    gate_wide(load_n(x + at, n), load_n(r + at, n), load_n(i + at, n), load_n(A + c, n), a, v);
     const f2 next = fma2(a, load_n(state + s, n), v);
     store2<false>(state + s, next, n);
     store2<false>(h + s, next, n);

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import block
-from test_block_gpu import BF, EPS, F32, _gen, _np, _rand, check
+from test_block_gpu import BF, EPS, F32, _decays, _gen, _np, _rand, check
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -193,3 +193,50 @@ def test_a_small_decay_of_a_step_keeps_its_precision(ssd, D, dtype):
     h = ssd.glr_decode_step(state, x[:, 0], r[:, 0], i[:, 0], A)
     check(h, ref[:, 0], bound[:, 0], "h")
     check(state, ref[:, 0], bound[:, 0], "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 62, 63])
+def test_a_nearly_shut_input_gate_lets_in_what_it_should(ssd, D, dtype):
+    """sigmoid(i) down to the end of the normal range, 1e-38, and nothing at all where the decay is exactly 1."""
+    i = torch.linspace(-86.0, -30.0, D).expand(1, 3, D).to(dtype).cuda().contiguous()
+    x = torch.full_like(i, 5120.0)
+    r = torch.full_like(i, 1.0)
+    r[0, 1] = -float("inf")  # a = 1: the state stays as it is, bit for bit
+    A = -torch.logspace(-3, 0, D).cuda()
+    args = [_np(v) for v in (x, r, i, A)]
+    ref, rlast, _ = block.glr(*args)
+    # exp(-i): its exponent is rounded at a magnitude of |i| log2 e and its factor is within U / 4 of log2 e, together
+    # 1.25 |i| U of the result; the other gate, the root and the decay of the state as GATE each.  1e-36 (in check): what
+    # lies below the normal range is flushed
+    rel = U * (110 + 3 * block.GATE)
+    h, last = ssd.glr_prefill(x, r, i, A)
+    check(h, ref, rel * np.abs(ref), "h")
+    check(last, rlast, rel * np.abs(rlast), "final state")
+    assert torch.equal(h[:, 1], h[:, 0])
+    state, one = torch.zeros(1, D, device="cuda"), []
+    for t in range(3):
+        one.append(ssd.glr_decode_step(state, x[:, t], r[:, t], i[:, t], A))
+    check(torch.stack(one, 1), ref, rel * np.abs(ref), "step")
+    check(state, rlast, rel * np.abs(rlast), "state")
+    assert torch.equal(one[1], one[0])
+    big = torch.full_like(x, 1e30)
+    assert (ssd.glr_prefill(big, torch.full_like(r, -float("inf")), torch.zeros_like(i), A)[0] == 0).all()
+    assert (ssd.glr_prefill(big, r, torch.zeros_like(i), torch.zeros_like(A))[0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,D", [(1, 1000, 64), (2, 37, 131), (40, 100, 70)])
+def test_nearly_shut_gates_among_open_ones(ssd, b, L, D, dtype):
+    """In the same tile and in neighbouring channels, in lone CTAs and in clusters."""
+    gen = _gen(b, L, D, 51)
+    x, r, i = (_rand(gen, b, L, D, dtype=dtype, std=1.5) for _ in range(3))
+    shut = torch.rand(b, L, D, generator=gen).cuda()
+    i[shut < 0.05] = -60.0
+    i[shut < 0.02] = -float("inf")
+    r[shut < 0.01] = -float("inf")
+    A, h0 = _decays(gen, D), _rand(gen, b, D)
+    h, last = ssd.glr_prefill(x, r, i, A, initial_state=h0)
+    ref, rlast, bound = block.glr(*(_np(v) for v in (x, r, i, A, h0)))
+    check(h, ref, bound, "h")
+    check(last, rlast, bound[:, -1], "final state")
