@@ -370,8 +370,10 @@ SSD_API ssd_status ssd_decode_window_flush(const ssd_dims *dims, ssd_dtype dtype
  * formed from expm1(L), so decays close to 1 lose nothing.  Arrays need only the
  * alignment of their elements; the wide-load path is taken when x, r, i, h (and their
  * gradients) are 16-byte aligned and dim and the strides are multiples of 16 bytes.
- * CTAs that share a long sequence wait for one another's part of a tile for at most 2 s;
- * after a wait that expired the channels concerned hold NaN from that tile on.
+ * CTAs that share a long sequence take its tiles in turn and wait for one another's part of
+ * each round of tiles for at most 2 s.  Where a wait expires, what would have depended on it
+ * is NaN: that CTA's tokens of the round, and all tokens of the sequence's 64 channels in every
+ * later round (in the order of the scan), with the state after them.  What is finite is right.
  */
 typedef struct {
   int64_t batch;       /* >= 0                                                           */
@@ -400,6 +402,18 @@ SSD_API ssd_status ssd_glr_prefill(const ssd_glr_dims *dims, ssd_dtype dtype, co
  */
 SSD_API ssd_status ssd_glr_decode_step(const ssd_glr_dims *dims, ssd_dtype dtype, float *state, const void *x,
                                        const void *r, const void *i, const float *A, void *h, ssd_stream_t stream);
+
+/*
+ * Self-test of that wait (the library's own check, as ssd_wait_selftest): the scans' exchange
+ * alone, over `tiles` (1 .. 64) rounds between `ranks` (2 .. 8) CTAs of 4 warps.  Every state
+ * starts at 1 and every warp's update adds 1; out [tiles, ranks, 4, 64] fp32 receives the state
+ * after each warp's.  Rank late_rank (-1: none) pauses delay_ns (0 .. 1e8) before round
+ * late_tile, and waits give up after limit_ns (1 .. 1e8).  Errors: SSD_ERR_INVALID_ARG for a
+ * value out of range, a NULL or misaligned out (8 bytes) or too few out_bytes; SSD_ERR_CUDA if
+ * the launch fails.
+ */
+SSD_API ssd_status ssd_glr_wait_selftest(float *out, size_t out_bytes, int ranks, int tiles, int late_rank,
+                                         int late_tile, uint64_t delay_ns, uint64_t limit_ns, ssd_stream_t stream);
 
 /*
  * Gradients of ssd_glr_prefill.  x, r, i, A and initial_state are its inputs and h its

@@ -115,6 +115,16 @@ ssd_status ssd_glr_decode_step(const ssd_glr_dims *dims, ssd_dtype dtype, float 
                                                        static_cast<bf16 *>(h), d, st));
 }
 
+ssd_status ssd_glr_wait_selftest(float *out, size_t out_bytes, int ranks, int tiles, int late_rank, int late_tile,
+                                 uint64_t delay_ns, uint64_t limit_ns, ssd_stream_t stream) {
+  if (ranks < 2 || ranks > 8 || tiles < 1 || tiles > 64 || late_rank < -1 || late_rank >= ranks || late_tile < 0 ||
+      late_tile >= tiles || delay_ns > 100000000ull || limit_ns == 0 || limit_ns > 100000000ull)
+    return SSD_ERR_INVALID_ARG;
+  if (!check_ptr(out, 1, 8) || out_bytes < (size_t)tiles * ranks * 4 * 64 * sizeof(float)) return SSD_ERR_INVALID_ARG;
+  return cuda_status(ssd::launch_glr_wait_selftest(out, ranks, tiles, late_rank, late_tile, delay_ns, limit_ns,
+                                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t ssd_glr_backward_workspace_size(const ssd_glr_dims *dims, ssd_dtype dtype) {
   GlrDims d;
   if (check_glr(dims, dtype, false, true, &d) != SSD_OK || d.b == 0 || d.L == 0) return 0;

@@ -239,6 +239,11 @@ __device__ __forceinline__ void sync_ranks() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void pause(uint64_t ns) {
+  const uint64_t t0 = sm100::globaltimer_ns();
+  while (sm100::globaltimer_ns() - t0 < ns) __nanosleep(10000);
+}
+
 // A state update h -> A h + H of a lane's two channels.
 struct alignas(16) Link {
   f2 A, H;
@@ -262,23 +267,29 @@ __device__ __forceinline__ Link load_link(const Link &l) {
 // The exchange of a tile: `publish` gives a warp's own update away, `collect` returns the state that enters its
 // tokens, `leave` ends the tile with the state after them; every warp of every rank calls each once a tile.  In a
 // cluster every warp keeps the state that enters the tile itself, from the updates of all ranks, so no tile waits for
-// the steps of the one before; in a lone CTA its last warp hands it on.  The ranks' updates travel as st.async messages that count themselves in on the receiver's mbarrier: no warp waits
-// for its own stores to drain, as it would at a cluster barrier a tile (2.7B-shaped bf16 prefill, 5 ranks: 47.8 us
-// against 52.6 us).  Two slots are enough: a rank sends tile k + 2 after it has collected k + 1, which every rank
-// published after all its warps had collected k.
-// A wait gives up after 2 s of global time; the state is then NaN from there on.
+// the steps of the one before; in a lone CTA its last warp hands it on.  The ranks' updates travel as st.async messages
+// that count themselves in on the receiver's mbarrier: no warp waits for its own stores to drain, as it would at a cluster
+// barrier a tile (2.7B-shaped bf16 prefill, 5 ranks: 47.8 us against 52.6 us).  Two slots are enough: a rank sends tile
+// k + 2 after it has collected k + 1, which every rank published after all its warps had collected k.
+// A wait gives up after kWaitLimit of global time.  What the lane forms from there on is NaN; at its CTA's next barrier
+// the whole CTA is lost: it waits and sends no more.  So it reuses no slot that may still be read, and every other rank
+// waits in vain at the next tile and is lost in turn: what is finite is right, and every later tile is NaN.
+constexpr uint64_t kWaitLimit = 2000000000ull;  // ns
 template <bool kCluster, int kW>
 struct Exchange {
   Links<kW> &l;
   int warp, lane, rank, ranks;
   int par, phase;  // of the tile
-  bool lost;       // a wait has expired
+  bool lost;       // a wait has expired: this lane's, or after a barrier any of the CTA
   Link before;     // the warps before this one
   f2 state;        // enters the tile
+  uint64_t limit;  // of a wait
 
   // All threads of all ranks, once: `enters` the first tile.
-  __device__ __forceinline__ Exchange(Links<kW> &links, int warp, int lane, int rank, int ranks, f2 enters)
-      : l(links), warp(warp), lane(lane), rank(rank), ranks(ranks), par(0), phase(0), lost(false), state(enters) {
+  __device__ __forceinline__ Exchange(Links<kW> &links, int warp, int lane, int rank, int ranks, f2 enters,
+                                      uint64_t limit = kWaitLimit)
+      : l(links), warp(warp), lane(lane), rank(rank), ranks(ranks), par(0), phase(0), lost(false), state(enters),
+        limit(limit) {
     if (!kCluster && warp == 0) l.carry[0][lane] = enters;
     if constexpr (kCluster) {
       if (threadIdx.x == 0) {
@@ -317,16 +328,19 @@ struct Exchange {
       if (ok) return true;
       const uint64_t t = sm100::globaltimer_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > 2000000000ull) return false;
+      if (t - t0 > limit) return false;
     }
   }
   __device__ __forceinline__ void publish(Link mine) {
     l.warp[par][warp][lane] = mine;
-    __syncthreads();
+    if constexpr (kCluster)
+      lost = __syncthreads_or(lost);
+    else
+      __syncthreads();
     before = {both(1.f), both(0.f)};
     for (int w = 0; w < warp; ++w) before = then(before, load_link(l.warp[par][w][lane]));
     if constexpr (kCluster) {
-      if (warp == kW - 1) {
+      if (warp == kW - 1 && !lost) {
         const Link all = then(before, mine);
         if (lane == 0) sm100::mbar_arrive_expect_tx(&l.arrived[par], 512u * ranks);
         for (int k = 0; k < ranks; ++k) send(k, all);
@@ -353,9 +367,14 @@ struct Exchange {
     par ^= 1;
   }
   __device__ __forceinline__ bool last() const { return warp == kW - 1 && rank == ranks - 1; }
-  // No rank leaves while another may still write to it.
-  __device__ __forceinline__ void finish() const {
-    if constexpr (kCluster) sync_ranks();
+  // No rank leaves while another may still write to it: each has collected all that was sent to it, but for a lost one,
+  // which gives the last messages, all sent before the barrier, a millisecond to land.
+  __device__ __forceinline__ void finish() {
+    if constexpr (kCluster) {
+      lost = __syncthreads_or(lost);
+      sync_ranks();
+      if (lost) pause(1000000);
+    }
   }
 };
 
@@ -639,6 +658,23 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   ex.finish();
 }
 
+// The exchange alone, with a limit and a rank that is late at one tile: every warp's update adds 1, and its state after
+// each tile goes to out [tile][rank][warp][kCh].
+__global__ void __launch_bounds__(4 * 32) k_glr_wait_selftest(float *out, int tiles, int late_rank, int late_tile,
+                                                              uint64_t delay, uint64_t limit) {
+  extern __shared__ __align__(16) char raw[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank(), ranks = cluster_size();
+  Exchange<true, 4> ex(*reinterpret_cast<Links<4> *>(raw), warp, lane, rank, ranks, both(1.f), limit);
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (rank == late_rank && tile == late_tile) pause(delay);
+    ex.publish({both(1.f), both(1.f)});
+    const f2 s = ex.collect() + both(1.f);
+    store2<true>(out + ((tile * ranks + rank) * 4 + warp) * kCh + 2 * lane, s, 2);
+    ex.leave(s);
+  }
+  ex.finish();
+}
+
 // Bytes of a copy that every array's rows allow: 16, 4, or 0 (elements of 2).  2.7B-shaped bf16 prefill: 47 us with 16;
 // two channels more, 62 us with 4; one more, 97 us by elements.
 template <typename T>
@@ -736,6 +772,21 @@ cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T
   const int64_t per = 128 * (w4 ? 4 : 2), blocks = (d.D + per - 1) / per;
   auto *f = w4 ? k_glr_decode<T, true> : k_glr_decode<T, false>;
   return launch_dependent(f, dim3((unsigned)(blocks * d.b)), 128, 0, st, state, x, r, i, A, h, d, (int)blocks);
+}
+
+cudaError_t launch_glr_wait_selftest(float *out, int ranks, int tiles, int late_rank, int late_tile, uint64_t delay,
+                                     uint64_t limit, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(4 * 32);
+  cfg.dynamicSmemBytes = sizeof(Links<4>) + 2 * ranks * 32 * sizeof(Link);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim = {(unsigned)ranks, 1, 1};
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_glr_wait_selftest, out, tiles, late_rank, late_tile, delay, limit);
 }
 
 // A row of dim for each batch row and rank, of which there are at most kMaxCtas blocks of kCh where ranks > 1.

@@ -90,6 +90,8 @@ cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *
 template <typename T>
 cudaError_t launch_glr_decode_step(float *state, const T *x, const T *r, const T *i, const float *A, T *h,
                                    const GlrDims &d, cudaStream_t st);
+cudaError_t launch_glr_wait_selftest(float *out, int ranks, int tiles, int late_rank, int late_tile, uint64_t delay,
+                                     uint64_t limit, cudaStream_t st);
 // floats of scratch: the partial sums of dA
 size_t glr_backward_floats(const GlrDims &d);
 template <typename T>

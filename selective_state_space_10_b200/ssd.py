@@ -48,7 +48,7 @@ EXPORTS = ("ssd_status_string", "ssd_version", "ssd_prefill_workspace_size",
            "ssd_prefill_noalloc_max_workspace", "ssd_prefill_noalloc_device_status", "ssd_decode_step",
            "ssd_frontend", "ssd_decode_window_step", "ssd_decode_window_flush", "ssd_wait_selftest",
            "ssd_prefill_host_buffer_size", "ssd_prefill_host", "ssd_glr_prefill", "ssd_glr_decode_step",
-           "ssd_glr_backward_workspace_size", "ssd_glr_backward", "ssd_residual_norm",
+           "ssd_glr_wait_selftest", "ssd_glr_backward_workspace_size", "ssd_glr_backward", "ssd_residual_norm",
            "ssd_norm_backward_workspace_size", "ssd_residual_norm_backward", "ssd_gated_norm",
            "ssd_gated_norm_backward")
 
@@ -109,6 +109,8 @@ def _load():
                        ("ssd_gated_norm_backward", [np_, ci, ci, ci, vp, vp, vp, f32] + [vp] * 5 + [sz, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ci
+    lib.ssd_glr_wait_selftest.argtypes = [fp, sz, ci, ci, ci, ci, ctypes.c_uint64, ctypes.c_uint64, vp]
+    lib.ssd_glr_wait_selftest.restype = ci
     lib.ssd_glr_backward_workspace_size.argtypes = [gp, ci]
     lib.ssd_glr_backward_workspace_size.restype = sz
     lib.ssd_norm_backward_workspace_size.argtypes = [np_]
@@ -627,6 +629,21 @@ def glr_decode_step(state, x, r, i, A, h=None, stream=None) -> torch.Tensor:
           (ctypes.byref(dims), _DTYPES[x.dtype], state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(),
            A.data_ptr(), h.data_ptr()))
     return h
+
+
+def glr_wait_selftest(ranks: int, tiles: int, late_rank: int = -1, late_tile: int = 0, delay_ns: int = 0,
+                      limit_ns: int = 100_000_000, out=None, stream=None) -> torch.Tensor:
+    """ssd_glr_wait_selftest: the state after every warp's update of 1, [tiles, ranks, 4, 64] fp32, from the scans'
+    exchange alone, with a rank that is late at one round and a limit of the waits."""
+    if out is None:
+        out = torch.empty((tiles, ranks, 4, 64), dtype=torch.float32, device="cuda")
+    if not out.is_cuda or out.dtype is not torch.float32 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous fp32 CUDA tensor")
+    st = lib.ssd_glr_wait_selftest(_ptr(out), out.numel() * 4, int(ranks), int(tiles), int(late_rank), int(late_tile),
+                                   int(delay_ns), int(limit_ns), _stream(stream))
+    if st != OK:
+        raise SSDError(st, "ssd_glr_wait_selftest")
+    return out
 
 
 def glr_backward(x, r, i, A, h, dh, initial_state=None, dfinal_state=None, dx=None, dr=None, di=None, dA=None,

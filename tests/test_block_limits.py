@@ -1,0 +1,26 @@
+"""Refusals of the gated linear recurrence and the norms at the limits of their calls, without a GPU."""
+import ctypes
+
+import pytest
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    from selective_state_space_10_b200 import build
+    build.build()
+    from selective_state_space_10_b200 import ssd as mod
+    return mod
+
+
+@pytest.mark.parametrize("bad", [dict(out=None), dict(out=FAKE + 4), dict(nbytes=6 * 4 * 4 * 64 * 4 - 1), dict(ranks=1),
+                                 dict(ranks=9), dict(tiles=0), dict(tiles=65), dict(late_rank=4), dict(late_rank=-2),
+                                 dict(late_tile=6), dict(late_tile=-1), dict(delay=100_000_001), dict(limit=0),
+                                 dict(limit=100_000_001)], ids=str)
+def test_wait_selftest_refusals(ssd, bad):
+    a = dict(out=FAKE, nbytes=1 << 30, ranks=4, tiles=6, late_rank=-1, late_tile=0, delay=0, limit=1000)
+    a.update(bad)
+    out = None if a["out"] is None else ctypes.c_void_p(a["out"])
+    assert ssd.lib.ssd_glr_wait_selftest(out, a["nbytes"], a["ranks"], a["tiles"], a["late_rank"], a["late_tile"],
+                                         a["delay"], a["limit"], None) == ssd.ERR_INVALID_ARG

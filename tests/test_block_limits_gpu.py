@@ -240,3 +240,27 @@ def test_nearly_shut_gates_among_open_ones(ssd, b, L, D, dtype):
     ref, rlast, bound = block.glr(*(_np(v) for v in (x, r, i, A, h0)))
     check(h, ref, bound, "h")
     check(last, rlast, bound[:, -1], "final state")
+
+
+@pytest.mark.parametrize("ranks", [2, 5, 8])
+def test_a_scan_whose_waits_hold(ssd, ranks):
+    """The self-test without a late rank, and with one that is late but within the limit: the sums of ones."""
+    want = torch.arange(2.0, 2 + 6 * ranks * 4, device="cuda").view(6, ranks, 4, 1).expand(6, ranks, 4, 64)
+    assert torch.equal(ssd.glr_wait_selftest(ranks, 6), want)
+    assert torch.equal(ssd.glr_wait_selftest(ranks, 6, late_rank=1, late_tile=2, delay_ns=2_000_000), want)
+
+
+@pytest.mark.parametrize("ranks,late_rank", [(2, 0), (2, 1), (5, 0), (5, 3), (8, 7)])
+@pytest.mark.parametrize("late_tile", [0, 1, 2, 4, 5])
+def test_a_scan_whose_wait_expires_leaves_nothing_wrong(ssd, ranks, late_rank, late_tile):
+    """A rank late by ten times the limit: before its round all is right; in that round its own states are, which wait for
+    ranks that came in time, and those of the ranks that gave up on it are NaN; after it everything is NaN, the last
+    rank's state included."""
+    want = torch.arange(2.0, 2 + 6 * ranks * 4, device="cuda").view(6, ranks, 4, 1).repeat(1, 1, 1, 64)
+    got = ssd.glr_wait_selftest(ranks, 6, late_rank, late_tile, delay_ns=40_000_000, limit_ns=4_000_000)
+    others = [k for k in range(ranks) if k != late_rank]
+    assert torch.equal(got[:late_tile], want[:late_tile])
+    assert torch.equal(got[late_tile, late_rank], want[late_tile, late_rank])
+    assert torch.isnan(got[late_tile, others]).all() and torch.isnan(got[late_tile + 1:]).all()
+    assert torch.equal(ssd.glr_wait_selftest(ranks, 6), torch.arange(2.0, 2 + 6 * ranks * 4, device="cuda").view(
+        6, ranks, 4, 1).expand(6, ranks, 4, 64))  # the next call is not touched by it
