@@ -173,6 +173,14 @@ def _check(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _scratch_bytes(t: torch.Tensor, name: str) -> int:
+    """The bytes of a scratch tensor.  A strided or expanded view has other memory between or behind its elements, which
+    the call would write."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def prefill(x, dt, A, B, C, D, chunk: int = 256, y=None, final_state=None, workspace=None,
             stream=None, events=None, initial_state=None, chunk_states=None):
     """Chunked prefill.  Returns (y fp32 [b,L,H,P], final_state fp32 [b,H,P,N]).
@@ -226,7 +234,7 @@ def prefill(x, dt, A, B, C, D, chunk: int = 256, y=None, final_state=None, works
     need = prefill_workspace_size(dims, dtype, chunk)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = 0 if workspace is None else _scratch_bytes(workspace, "workspace")
     if extended:
         st = lib.ssd_prefill_ex(ctypes.byref(dims), dtype, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                 int(chunk), _ptr(initial_state), _ptr(y), _ptr(final_state),
@@ -284,7 +292,7 @@ def prefill_host(x, dt, A, B, C, D, chunk: int = 256, y=None, final_state=None, 
         raise ValueError("device_buffer must be a CUDA tensor")
     st = lib.ssd_prefill_host(ctypes.byref(dims), dtype, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                               int(chunk), _ptr(y), _ptr(final_state), _ptr(device_buffer),
-                              device_buffer.numel() * device_buffer.element_size(), _stream(stream))
+                              _scratch_bytes(device_buffer, "device_buffer"), _stream(stream))
     if st != OK:
         raise SSDError(st, "ssd_prefill_host")
     return y, final_state
@@ -576,7 +584,7 @@ def _workspace(workspace, need: int, like: torch.Tensor):
         return like.new_empty(need, dtype=torch.uint8), need
     if workspace.device != like.device:
         raise ValueError(f"workspace is on {workspace.device}, expected {like.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, _scratch_bytes(workspace, "workspace")
 
 
 def glr_prefill(x, r, i, A, initial_state=None, h=None, final_state=None, stream=None):

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 FAKE = 1 << 20
 
@@ -24,3 +25,19 @@ def test_wait_selftest_refusals(ssd, bad):
     out = None if a["out"] is None else ctypes.c_void_p(a["out"])
     assert ssd.lib.ssd_glr_wait_selftest(out, a["nbytes"], a["ranks"], a["tiles"], a["late_rank"], a["late_tile"],
                                          a["delay"], a["limit"], None) == ssd.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("view", [torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(64, 64)[:, :32],
+                                  torch.empty(64, dtype=torch.uint8)[::2]], ids=["expanded", "columns", "strided"])
+def test_scratch_that_is_a_view_with_gaps_is_refused(ssd, view):
+    """Its bytes are not where the call would write them."""
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        ssd._workspace(view, 16, torch.empty(1))
+    with pytest.raises(ValueError, match="device_buffer must be contiguous"):
+        ssd._scratch_bytes(view, "device_buffer")
+
+
+def test_scratch_that_is_whole_is_taken(ssd):
+    for t in (torch.empty(64, dtype=torch.uint8)[16:], torch.empty(4, 4), torch.empty(0, dtype=torch.uint8)):
+        got, nbytes = ssd._workspace(t, 16, torch.empty(1))
+        assert got is t and nbytes == t.numel() * t.element_size()
