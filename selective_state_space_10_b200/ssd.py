@@ -512,8 +512,12 @@ def _call(fn, dev: int, args) -> None:
 def _on(stream, like: torch.Tensor, fn, *args):
     """fn(*args) with `stream` (a torch stream or a handle) current, so that what fn allocates
     is that stream's memory too: nothing of it is reused before the stream has passed the call."""
+    if not like.is_cuda:
+        raise ValueError("libssd runs on CUDA tensors only")
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    elif stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, expected {like.device}")
     with torch.cuda.stream(stream):
         return fn(*args)
 

@@ -1,5 +1,6 @@
 """Refusals of the gated linear recurrence and the norms at the limits of their calls, without a GPU."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -41,3 +42,17 @@ def test_scratch_that_is_whole_is_taken(ssd):
     for t in (torch.empty(64, dtype=torch.uint8)[16:], torch.empty(4, 4), torch.empty(0, dtype=torch.uint8)):
         got, nbytes = ssd._workspace(t, 16, torch.empty(1))
         assert got is t and nbytes == t.numel() * t.element_size()
+
+
+def test_a_stream_of_another_device_is_refused(ssd):
+    """The call would have run on the current stream of the tensors' device, not on the one given."""
+    ran = []
+    on0 = SimpleNamespace(is_cuda=True, device=torch.device("cuda", 0))
+    stream1 = SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:1, expected cuda:0"):
+        ssd._on(stream1, on0, ran.append, 1)
+    t = torch.zeros(1, 3, 8)
+    for stream in (0, stream1):
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            ssd.glr_prefill(t, t, t, torch.zeros(8), stream=stream)
+    assert not ran
