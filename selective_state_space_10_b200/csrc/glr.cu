@@ -4,12 +4,13 @@
 //
 // over whole sequences, for one token, and its gradients.
 #include <algorithm>
-#include <atomic>
 #include <initializer_list>
+#include <type_traits>
 
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels.h"
+#include "per_device.h"
 #include "sm100.cuh"
 
 namespace ssd {
@@ -686,6 +687,14 @@ int copy_width(std::initializer_list<const void *> arrays, std::initializer_list
     while (width > 0 && s * (int64_t)sizeof(T) % width != 0) width = width == 16 ? 4 : 0;
   return width;
 }
+// run(std::integral_constant) for a width; elements of 4 bytes are aligned to 4.
+template <typename T, typename F>
+cudaError_t by_width(int width, F run) {
+  if (width == 16) return run(std::integral_constant<int, 16>{});
+  if constexpr (sizeof(T) == 2)
+    if (width == 0) return run(std::integral_constant<int, 0>{});
+  return run(std::integral_constant<int, 4>{});
+}
 bool wide(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // The launch of a scan kernel: `ranks` CTAs share a sequence and are a cluster.  The kernel's limits are set to the same
@@ -712,33 +721,35 @@ cudaError_t set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], F *f, 
 // How many CTAs share a sequence: the most, up to kMaxRanks, one a tile and kMaxCtas in all, whose clusters the GPU
 // holds at once.
 // What it holds depends on how clusters of a size fill its graphics clusters (2.7B-shaped prefill, 80 blocks of
-// channels: 5 ranks 47.9 us, 4 56.0 us; 6 need a second wave, 59.6 us), so each kernel asks the runtime once.
-template <typename T, int N, int kW, int kT, typename... P>
-cudaError_t pick_ranks(void (*many)(P...), int64_t ctas, int64_t L, int &ranks) {
-  static std::atomic<int> held[kMaxRanks + 1];  // clusters of each size that fit, + 1; 0: not asked yet
+// channels: 5 ranks 47.9 us, 4 56.0 us; 6 need a second wave, 59.6 us), so the runtime is asked, once for each kernel,
+// size of a cluster and device.
+template <typename T, int N, int kW, int kT, auto *many>
+cudaError_t pick_ranks(int64_t ctas, int64_t L, int &ranks) {
   ranks = (int)std::min<int64_t>((L + kW * kT - 1) / (kW * kT), kMaxRanks);
   for (; ranks > 1; --ranks) {
     if (ctas * ranks > kMaxCtas) continue;
-    int fit = held[ranks].load(std::memory_order_relaxed) - 1;
-    if (fit < 0) {
+    int fit = 0;
+    const cudaError_t e = clusters_held<many, kMaxRanks + 1>(ranks).get(fit, [&](int &clusters) {
       cudaLaunchConfig_t cfg;
       cudaLaunchAttribute at[2];
-      cudaError_t e = set_up<T, N, kW, kT>(cfg, at, many, 1, ranks, nullptr);
-      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, many, &cfg);
-      if (e != cudaSuccess) return e;
-      held[ranks].store(fit + 1, std::memory_order_relaxed);
-    }
+      const cudaError_t e = set_up<T, N, kW, kT>(cfg, at, many, 1, ranks, nullptr);
+      return e != cudaSuccess ? e : cudaOccupancyMaxActiveClusters(&clusters, many, &cfg);
+    });
+    if (e != cudaSuccess) return e;
     if (ctas <= fit) break;
   }
   return cudaSuccess;
 }
 
-template <typename T, int N, int kW, int kT, typename... P, typename... V>
-cudaError_t launch_scan(void (*one)(P...), void (*many)(P...), int64_t ctas, int ranks, cudaStream_t st, V... v) {
+// `one`: the kernel of a lone CTA a sequence, `many`: of a cluster.  ranks: CTAs a sequence, as picked.
+template <typename T, int N, int kW, int kT, auto *one, auto *many, typename... V>
+cudaError_t launch_scan(int64_t ctas, int64_t L, int &ranks, cudaStream_t st, V... v) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute at[2];
+  cudaError_t e = pick_ranks<T, N, kW, kT, many>(ctas, L, ranks);
+  if (e != cudaSuccess) return e;
   auto *f = ranks > 1 ? many : one;
-  cudaError_t e = set_up<T, N, kW, kT>(cfg, at, f, ctas, ranks, st);
+  e = set_up<T, N, kW, kT>(cfg, at, f, ctas, ranks, st);
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, f, v...);
 }
 
@@ -748,21 +759,15 @@ template <typename T>
 cudaError_t launch_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h,
                                float *final_state, const GlrDims &d, cudaStream_t st) {
   const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
-  const int width = copy_width<T>({x, r, i, h}, {d.D, d.row});
   using Shape = PrefillShape<T>;
   constexpr int W = Shape::W, N = Shape::N;
-  auto run = [&](auto *one, auto *many) {
-    int ranks;
-    cudaError_t e = pick_ranks<T, 3, W, N>(many, ctas, d.L, ranks);
-    if (e != cudaSuccess) return e;
-    return launch_scan<T, 3, W, N>(one, many, ctas, ranks, st, x, r, i, A, init, h, final_state, d, (int)blocks);
+  int ranks;
+  auto run = [&](auto width) {
+    constexpr int CW = decltype(width)::value;
+    return launch_scan<T, 3, W, N, k_glr_prefill<T, CW, false, W, N>, k_glr_prefill<T, CW, true, W, N>>(
+        ctas, d.L, ranks, st, x, r, i, A, init, h, final_state, d, (int)blocks);
   };
-  switch (width) {
-    case 16: return run(k_glr_prefill<T, 16, false, W, N>, k_glr_prefill<T, 16, true, W, N>);
-    case 4: return run(k_glr_prefill<T, 4, false, W, N>, k_glr_prefill<T, 4, true, W, N>);
-  }
-  if constexpr (sizeof(T) == 2) return run(k_glr_prefill<T, 0, false, W, N>, k_glr_prefill<T, 0, true, W, N>);
-  return cudaErrorInvalidValue;
+  return by_width<T>(copy_width<T>({x, r, i, h}, {d.D, d.row}), run);
 }
 
 template <typename T>
@@ -797,20 +802,15 @@ cudaError_t launch_glr_backward(const T *x, const T *r, const T *i, const float 
                                 const T *dh, const float *dfinal, T *dx, T *dr, T *di, float *dA, float *dinit,
                                 float *part, const GlrDims &d, cudaStream_t st) {
   const int64_t blocks = (d.D + kCh - 1) / kCh, ctas = blocks * d.b;
-  const int width = copy_width<T>({x, r, i, h, dh, dx, dr, di}, {d.D, d.row, d.grad});
   using Shape = BackwardShape<T>;
   constexpr int W = Shape::W, N = Shape::N;
-  int ranks = 1;
-  auto run = [&](auto *one, auto *many) {
-    cudaError_t e = pick_ranks<T, 5, W, N>(many, ctas, d.L, ranks);
-    if (e != cudaSuccess) return e;
-    return launch_scan<T, 5, W, N>(one, many, ctas, ranks, st, x, r, i, A, init, h, dh, dfinal, dx, dr, di, dinit, part, d,
-                                   (int)blocks);
+  int ranks;
+  auto run = [&](auto width) {
+    constexpr int CW = decltype(width)::value;
+    return launch_scan<T, 5, W, N, k_glr_backward<T, CW, false, W, N>, k_glr_backward<T, CW, true, W, N>>(
+        ctas, d.L, ranks, st, x, r, i, A, init, h, dh, dfinal, dx, dr, di, dinit, part, d, (int)blocks);
   };
-  cudaError_t e = cudaErrorInvalidValue;
-  if (width == 16) e = run(k_glr_backward<T, 16, false, W, N>, k_glr_backward<T, 16, true, W, N>);
-  else if (width == 4) e = run(k_glr_backward<T, 4, false, W, N>, k_glr_backward<T, 4, true, W, N>);
-  else if constexpr (sizeof(T) == 2) e = run(k_glr_backward<T, 0, false, W, N>, k_glr_backward<T, 0, true, W, N>);
+  const cudaError_t e = by_width<T>(copy_width<T>({x, r, i, h, dh, dx, dr, di}, {d.D, d.row, d.grad}), run);
   if (e != cudaSuccess) return e;
   return launch_row_sums(part, nullptr, dA, nullptr, d.D, d.b * ranks, st);
 }

@@ -1,5 +1,7 @@
 """Refusals of the gated linear recurrence and the norms at the limits of their calls, without a GPU."""
 import ctypes
+import os
+import subprocess
 from types import SimpleNamespace
 
 import pytest
@@ -56,3 +58,14 @@ def test_a_stream_of_another_device_is_refused(ssd):
         with pytest.raises(ValueError, match="CUDA tensors only"):
             ssd.glr_prefill(t, t, t, torch.zeros(8), stream=stream)
     assert not ran
+
+
+def test_what_the_runtime_says_is_kept_by_kernel_and_device(tmp_path):
+    here = os.path.dirname(os.path.abspath(__file__))
+    csrc = os.path.join(os.path.dirname(here), "selective_state_space_10_b200", "csrc")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc"))), "include")
+    exe = str(tmp_path / "per_device_test")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I" + csrc, "-I" + cuda, os.path.join(here, "per_device_test.cpp"), "-o", exe],
+                   check=True)
+    done = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0, done.stdout
