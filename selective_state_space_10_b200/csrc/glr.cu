@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
     f2 args = both(0.f);
 #pragma unroll
     for (int j = 0; j < kT; ++j) gate(at(0, j), at(1, j), at(2, j), Ac, a[j], v[j], args);
-    if (!finite(args)) wide_terms(in, p.lane, Ac, v);
+    if (rest > 0 && !finite(args)) wide_terms(in, p.lane, Ac, v);  // past the end there is whatever the tile held before
     if (rest < kT) {  // the sequence ends within these tokens: the rest leave the state as it is
 #pragma unroll
       for (int j = 0; j < kT; ++j)
