@@ -441,9 +441,8 @@ __device__ __forceinline__ void wide_terms(T (&in)[3][kT][kCh], int lane, f2 A, 
 // (a second set of registers, 8 warps an SM) measured 64 us.
 template <typename T, int CW, bool kCluster, int kW, int kT>
 __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
-    k_glr_prefill(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
-                  const float *__restrict__ A, const float *init, T *__restrict__ h, float *final_state, GlrDims d,
-                  int blocks) {
+    k_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h, float *final_state,
+                  GlrDims d, int blocks) {
   constexpr int kTile = kW * kT;
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 3, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 3, kW, kT> *>(raw);
@@ -525,10 +524,8 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
 // One token: 4 channels a thread in wide words (kWide), else two by elements.  256 x 5120 bf16 (21 MB, inside L2): 5.1 us
 // on the device, 7.2 us by elements; a call takes the host longer than that.
 template <typename T, bool kWide>
-__global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, const T *__restrict__ x,
-                                                    const T *__restrict__ r, const T *__restrict__ i,
-                                                    const float *__restrict__ A, T *__restrict__ h, GlrDims d,
-                                                    int blocks) {
+__global__ void __launch_bounds__(128) k_glr_decode(float *state, const T *x, const T *r, const T *i,
+                                                    const float *A, T *h, GlrDims d, int blocks) {
   constexpr int E = kWide ? 4 : 2;
   sm100::grid_dep_launch();
   sm100::grid_dep_wait();
@@ -565,10 +562,8 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *__restrict__ state, c
 // 1.61 GB, 4.3 TB/s, 66 % of the measured copy bandwidth; issue slots 53 % busy, as in the forward scan.
 template <typename T, int CW, bool kCluster, int kW, int kT>
 __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
-    k_glr_backward(const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
-                   const float *__restrict__ A, const float *__restrict__ init, const T *__restrict__ h,
-                   const T *__restrict__ dh, const float *dfinal, T *__restrict__ dx, T *__restrict__ dr,
-                   T *__restrict__ di, float *dinit, float *__restrict__ part, GlrDims d, int blocks) {
+    k_glr_backward(const T *x, const T *r, const T *i, const float *A, const float *init, const T *h, const T *dh,
+                   const float *dfinal, T *dx, T *dr, T *di, float *dinit, float *part, GlrDims d, int blocks) {
   constexpr int kTile = kW * kT;
   extern __shared__ __align__(16) char raw[];
   ScanSmem<T, 5, kW, kT> &sm = *reinterpret_cast<ScanSmem<T, 5, kW, kT> *>(raw);

@@ -27,6 +27,8 @@ cudaError_t launch(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStr
 
 // The same as a programmatic dependent of what the stream ran before: its CTAs take their places as the last ones of
 // that kernel leave theirs, and f itself waits (grid_dep_wait, before it touches memory) until that kernel is complete.
+// f's pointers are not __restrict__: what they point to may change until that wait, and the qualifier would let the
+// compiler load it before, or as data that is read-only for all of the kernel.
 template <typename... P, typename... V>
 cudaError_t launch_dependent(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, V... v) {
   return launch(f, grid, threads, smem, st, true, v...);

@@ -1,6 +1,7 @@
 """Refusals of the gated linear recurrence and the norms at the limits of their calls, without a GPU."""
 import ctypes
 import os
+import re
 import subprocess
 from types import SimpleNamespace
 
@@ -69,3 +70,21 @@ def test_what_the_runtime_says_is_kept_by_kernel_and_device(tmp_path):
                    check=True)
     done = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert done.returncode == 0, done.stdout
+
+
+def test_kernels_that_start_early_promise_nothing_of_their_memory():
+    """A kernel that waits for the one before it may not have __restrict__ pointers: the memory behind them changes until
+    the wait, and the qualifier allows loads before it."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "selective_state_space_10_b200", "csrc")
+    early = []
+    for name in ("glr.cu", "norm.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for kernel in re.split(r"(?=__global__ void)", text)[1:]:
+            head, body = kernel.split("{", 1)
+            body = body[:body.index("\n}")]
+            if "grid_dep_wait" in body:
+                early.append(re.search(r"(k_\w+)\(", head).group(1))
+                assert "__restrict__" not in head, early[-1]
+    assert sorted(early) == ["k_glr_backward", "k_glr_decode", "k_glr_prefill", "k_norm_backward_rows", "k_norm_rows",
+                             "k_row_sums"]
