@@ -63,18 +63,18 @@ __device__ __forceinline__ void decay(f2 L, f2 &a, f2 &v) {
 }
 
 // One step: the decay a and the input term b = sqrt(1 - a^2) sigmoid(i) x, with rest = 1 - a^2 and o = 1 + exp(-i) as
-// x rest / sqrt(rest o^2): one root in place of a root and a reciprocal.  kTiny leaves b exactly 0 where a is 1, and
-// changes nothing from rest = 2e-31 on.  Where the root's argument overflows (i below -44) its sum in `args` is no longer
-// finite, and gate_wide has to be taken.
+// x rest / sqrt(rest o^2): one root in place of a root and a reciprocal.  kTiny leaves b exactly 0 where a is 1 or o
+// infinite, and changes nothing from rest = 2e-31 on.  Where the root's argument overflows (i below -44) its sum in `args`
+// is no longer finite, and b is 0: right for a shut gate, but a nearly shut one has to take gate_wide.
 __device__ __forceinline__ void gate(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b, f2 &args) {
   f2 v;
   decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
-  const f2 rest = fma2(v, a, v), o = exp_neg(i) + both(1.f), arg = fma2(o * o, rest, both(kTiny));
+  const f2 rest = fma2(v, a, v), o = exp_neg(i) + both(1.f), arg = o * o * (rest + both(kTiny));
   b = x * (rest * rsqrt_approx(arg));
   args = args + arg;
 }
 // The same for every i: a sigmoid down to the end of the normal range.  Its fifth special function for every token would
-// take the 2.7B-shaped bf16 prefill to 50.3 us; the sum of the arguments, and this where it says so, 48.0 us.
+// take the 2.7B-shaped bf16 prefill to 50.3 us; the sum of the arguments, and this where it is needed, 48.1 us.
 __device__ __forceinline__ void gate_wide(f2 x, f2 r, f2 i, f2 A, f2 &a, f2 &b) {
   f2 v;
   decay(A * rcp(exp_neg(r) + both(1.f)), a, v);
@@ -411,24 +411,29 @@ __device__ __forceinline__ Place place(int64_t D, int blocks) {
   return p;
 }
 
-// The input terms of a warp's tokens once more, by gate_wide (a scan's lane whose gate found a nearly shut input gate).  A
-// loop of one token at a time leaves each term in the lane's own words of the tile, so that it takes no registers beside
-// the decays.
+// The input terms of a warp's tokens where a gate of the lane's may be nearly shut (its sum of arguments is not finite).
+// Below kShut, where masks put a gate, the term is 0 already; up to kNearlyShut the terms take gate_wide, in a loop of one
+// token at a time that leaves each term in the lane's own words of the tile and so takes no registers beside the decays.
+// 2.7B-shaped bf16 prefill with one gate in 20 masked 50.8 us, all masked 51.8 us, all at -60 90 us.
+constexpr float kShut = -87.4f, kNearlyShut = -44.f;  // 1 + exp(-i) is 2^126, its square 2^127
 template <typename T, int kT>
-__device__ __forceinline__ void wide_loop(T (*in)[kT][kCh], int lane, f2 A) {
+__device__ __forceinline__ void shut_terms(T (&in)[3][kT][kCh], int lane, f2 A, f2 (&b)[kT]) {
+  bool nearly = false;
+#pragma unroll 4
+  for (int j = 0; j < kT; ++j) {
+    const float2 i = split(load2(&in[2][j][2 * lane]));
+    nearly = nearly || (i.x >= kShut && i.x <= kNearlyShut) || (i.y >= kShut && i.y <= kNearlyShut);
+  }
+  if (!nearly) return;
 #pragma unroll 1
   for (int j = 0; j < kT; ++j) {
-    T *x = &in[0][j][2 * lane], *r = &in[1][j][2 * lane], *i = &in[2][j][2 * lane];
-    f2 a, b;
-    gate_wide(load2(x), load2(r), load2(i), A, a, b);
-    const float2 s = split(b);
+    T *x = &in[0][j][2 * lane], *i = &in[2][j][2 * lane];
+    f2 a, term;
+    gate_wide(load2(x), load2(&in[1][j][2 * lane]), load2(i), A, a, term);
+    const float2 s = split(term);
     *reinterpret_cast<float *>(x) = s.x;
     *reinterpret_cast<float *>(i) = s.y;
   }
-}
-template <typename T, int kT>
-__device__ __forceinline__ void wide_terms(T (&in)[3][kT][kCh], int lane, f2 A, f2 (&b)[kT]) {
-  wide_loop<T, kT>(in, lane, A);
 #pragma unroll
   for (int j = 0; j < kT; ++j)
     b[j] = mk(*reinterpret_cast<const float *>(&in[0][j][2 * lane]), *reinterpret_cast<const float *>(&in[2][j][2 * lane]));
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
     f2 args = both(0.f);
 #pragma unroll
     for (int j = 0; j < kT; ++j) gate(at(0, j), at(1, j), at(2, j), Ac, a[j], v[j], args);
-    if (rest > 0 && !finite(args)) wide_terms(in, p.lane, Ac, v);  // past the end there is whatever the tile held before
+    if (rest > 0 && !finite(args)) shut_terms(in, p.lane, Ac, v);  // past the end there is whatever the tile held before
     if (rest < kT) {  // the sequence ends within these tokens: the rest leave the state as it is
 #pragma unroll
       for (int j = 0; j < kT; ++j)

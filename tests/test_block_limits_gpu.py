@@ -264,3 +264,31 @@ def test_a_scan_whose_wait_expires_leaves_nothing_wrong(ssd, ranks, late_rank, l
     assert torch.isnan(got[late_tile, others]).all() and torch.isnan(got[late_tile + 1:]).all()
     assert torch.equal(ssd.glr_wait_selftest(ranks, 6), torch.arange(2.0, 2 + 6 * ranks * 4, device="cuda").view(
         6, ranks, 4, 1).expand(6, ranks, 4, 64))  # the next call is not touched by it
+
+
+@pytest.mark.parametrize("mask", [-1e4, -float("inf"), "lowest"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,D", [(1, 1000, 64), (3, 50, 74), (2, 21, 33)])
+def test_masked_tokens_leave_the_state_as_it_is(ssd, b, L, D, dtype, mask):
+    """Both gates masked at single tokens and at a padded end: every token gets what it gets in a sequence without the
+    masked ones, a masked one what the last token before it got.  (Not bit for bit: the state that enters a warp's tokens
+    is a sum grouped otherwise than the steps before it, so both are within the last token's bound.  Before the first
+    token, and in single steps, nothing is rounded.)"""
+    gen = _gen(b, L, D, 61)
+    x, r, i = (_rand(gen, b, L, D, dtype=dtype, std=1.5) for _ in range(3))
+    off = torch.rand(L, generator=gen) < 0.3
+    off[L - L // 4:] = True
+    low = torch.finfo(dtype).min if mask == "lowest" else mask
+    r[:, off.cuda()], i[:, off.cuda()] = low, low
+    A, h0 = _decays(gen, D), _rand(gen, b, D)
+    h, last = ssd.glr_prefill(x, r, i, A, initial_state=h0)
+    on = (~off).nonzero()[:, 0].cuda()
+    ref, rlast, bound = block.glr(*(_np(v[:, on]) for v in (x, r, i)), _np(A), _np(h0))
+    seen = np.cumsum(~off.numpy())  # tokens up to and with each one that are not masked; 0: the initial state
+    ref, bound = np.concatenate([_np(h0)[:, None], ref], 1), np.concatenate([0 * _np(h0)[:, None], bound], 1)
+    check(h, ref[:, seen], bound[:, seen], "h")
+    check(last, rlast, bound[:, -1], "final state")
+    state = h0.clone()
+    for t in off.nonzero()[:3, 0].tolist():
+        out = ssd.glr_decode_step(state, x[:, t], r[:, t], i[:, t], A)
+        assert torch.equal(state, h0) and torch.equal(out, h0.to(dtype))
