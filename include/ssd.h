@@ -367,7 +367,9 @@ SSD_API ssd_status ssd_decode_window_flush(const ssd_dims *dims, ssd_dtype dtype
  *   states    [batch, dim] fp32
  *
  * fp32 arithmetic for both dtypes; bf16 outputs are rounded to nearest even.  1 - a^2 is
- * formed from expm1(L), so decays close to 1 lose nothing.  Arrays need only the
+ * formed from expm1(L), so decays close to 1 lose nothing, and small ones keep their own
+ * precision.  A decay or sigmoid below the normal range of fp32 counts as 0 to 1.7e-38.
+ * Arrays need only the
  * alignment of their elements; the wide-load path is taken when x, r, i, h (and their
  * gradients) are 16-byte aligned and dim and the strides are multiples of 16 bytes.
  * CTAs that share a long sequence take its tiles in turn and wait for one another's part of
@@ -388,8 +390,9 @@ typedef struct {
  * receives h_{seqlen-1} in fp32 (initial_state, or zero, when seqlen == 0) and may be
  * initial_state itself (updated in place).  Pieces of a prompt continue from one another's
  * final_state.  Errors: SSD_ERR_INVALID_ARG for NULL dims, negative sizes, dim < 1, a
- * stride below dim, NULL or misaligned non-empty arrays, and batch * ceil(dim / 64) above
- * 2^28 (the launch grid); SSD_ERR_CUDA if a launch fails.
+ * stride below dim, NULL or misaligned non-empty arrays, batch * ceil(dim / 64) of 2^28 or
+ * more (the launch grid), a size above 2^30 or an array that spans more than 4e12 elements;
+ * SSD_ERR_CUDA if a launch fails.
  */
 SSD_API ssd_status ssd_glr_prefill(const ssd_glr_dims *dims, ssd_dtype dtype, const void *x, const void *r,
                                    const void *i, const float *A, const float *initial_state, void *h,
@@ -469,8 +472,8 @@ typedef struct {
  * x and out in `dtype`, residual and residual_out in `residual_dtype`: the same or fp32
  * (otherwise SSD_ERR_UNSUPPORTED).  residual_out may be residual (updated in place); out is
  * formed from the unrounded s.  Errors: SSD_ERR_INVALID_ARG for NULL dims, bad sizes (rows *
- * ngroups above 2^31 - 1 among them) or types, eps not positive and finite, NULL or
- * misaligned non-empty arrays.
+ * ngroups above 2^31 - 1, dim above 2^30 and arrays that span more than 4e12 elements among
+ * them) or types, eps not positive and finite, NULL or misaligned non-empty arrays.
  */
 SSD_API ssd_status ssd_residual_norm(const ssd_norm_dims *dims, ssd_dtype dtype, ssd_dtype residual_dtype,
                                      const void *x, const float *scale, const void *residual, const float *weight,

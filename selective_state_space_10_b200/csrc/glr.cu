@@ -38,7 +38,7 @@ __device__ __forceinline__ f2 exp_neg_finite(f2 v) {
 }
 
 // a = exp(L) and v = 1 - a for L <= 0, both to full relative precision: L = n ln 2 + f with |f| <= ln 2 / 2,
-// p = 1 - exp(f) by a polynomial (fitted with relative weights and p'(0) = -1; 1.6e-8 off at most, below half a
+// p = 1 - exp(f) by a polynomial (fitted with relative weights, with 1 and 1/2 kept; 1.8e-8 off at most, below half a
 // step of fp32), a = 2^n (1 - p), v = (1 - 2^n) + 2^n p.  1 - a^2 = v (1 + a) then loses nothing for decays close
 // to 1; an exp(L) rounded near 1 and subtracted would, and its error would be carried through every step of a
 // long memory.  Nor is a formed as 1 - v, which would leave a small one the absolute precision of 1.  The exponential
@@ -143,10 +143,10 @@ __device__ __forceinline__ void store2(T *p, f2 f, int n) {
 // of CTAs shares a sequence, a tile each in turn: the CTAs' own A h + H go to the ranks behind
 // them through distributed shared memory.
 // Warps, tokens a warp and CTAs an SM of each scan.  Long runs of tokens amortise a tile's exchange, small CTAs keep the
-// SMs evenly loaded (2.7B-shaped bf16 prefill: 4 x 16 47.8 us, 4 x 12 54.0, 4 x 8 54.3, 2 x 16 57.2, 8 x 16 66.5 us;
-// long-context bf16 gradient: 4 x 12 381 us, 4 x 8 408, 2 x 12 437, 4 x 4 490, 8 x 8 509 us, before the last step).  fp32 tiles are twice
-// the bytes; the prefill runs the same with any of these shapes, and the gradient's short runs leave room for four CTAs
-// (b = 4, L = 4096, D = 5120: 4 x 4 442 us, 4 x 8 507 us; b = 1, L = 16384, D = 1536: 182 and 150 us).
+// SMs evenly loaded (before the last steps; 2.7B-shaped bf16 prefill: 4 x 16 47.8 us, 4 x 12 54.0, 4 x 8 54.3, 2 x 16 57.2,
+// 8 x 16 66.5 us; long-context bf16 gradient: 4 x 12 381 us, 4 x 8 408, 2 x 12 437, 4 x 4 490, 8 x 8 509 us).  fp32 tiles are
+// twice the bytes; the prefill runs the same with any of these shapes, and the gradient's short runs leave room for four
+// CTAs (b = 4, L = 4096, D = 5120: 4 x 4 442 us, 4 x 8 507 us; b = 1, L = 16384, D = 1536: 182 and 150 us).
 template <typename T>
 struct PrefillShape {
   static constexpr int W = 4, N = sizeof(T) == 2 ? 16 : 8, kResident = 3;
@@ -439,11 +439,12 @@ __device__ __forceinline__ void shut_terms(T (&in)[3][kT][kCh], int lane, f2 A, 
     b[j] = mk(*reinterpret_cast<const float *>(&in[0][j][2 * lane]), *reinterpret_cast<const float *>(&in[2][j][2 * lane]));
 }
 
-// The forward scan.  2.7B-shaped bf16 layer (b = 1, L = 4096, D = 5120): 47.4 us for 168 MB, 3.5 TB/s, 54 % of the
-// measured copy bandwidth; fp32 55.7 us, 6.0 TB/s.  The bf16 scan has twice the elements a byte: 35 warp instructions and
-// 4 special functions for each, issue slots 50 % and special-function units 46 % busy with the 10 warps an SM that 160
-// registers leave; what remains is their latency.  Forming the next tile's gates while a tile's exchange is under way
-// (a second set of registers, 8 warps an SM) measured 64 us.
+// The forward scan.  2.7B-shaped bf16 layer (b = 1, L = 4096, D = 5120): 48.1 us a call for 168 MB, 3.5 TB/s, 53 % of the
+// measured copy bandwidth; fp32 57.2 us, 5.9 TB/s.  The bf16 scan has twice the elements a byte: 37 warp instructions and
+// 4 special functions for each, issue slots 53 % and special-function units 46 % busy with the 10 warps an SM that 166
+// registers leave; what remains is their latency, and that a tile is serial within its CTA: gates, barrier, messages,
+// steps.  Forming the next tile's gates while a tile's exchange is under way (a second set of registers, 8 warps an SM)
+// measured 64 us.
 template <typename T, int CW, bool kCluster, int kW, int kT>
 __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
     k_glr_prefill(const T *x, const T *r, const T *i, const float *A, const float *init, T *h, float *final_state,
@@ -526,8 +527,9 @@ __global__ void __launch_bounds__(kW * 32, PrefillShape<T>::kResident)
   ex.finish();
 }
 
-// One token: 4 channels a thread in wide words (kWide), else two by elements.  256 x 5120 bf16 (21 MB, inside L2): 5.1 us
-// on the device, 7.2 us by elements; a call takes the host longer than that.
+// One token: 4 channels a thread in wide words (kWide), else two by elements.  256 x 5120 bf16 (21 MB read and written) in
+// a graph of such steps: 3.7 us a step on the same arrays, which stay in L2, 4.7 us on eight sets in turn, 6.2 us by
+// elements (5121 channels); 6.4 us alone and with the clocks that a profiler finds.  A call takes the host longer.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(128) k_glr_decode(float *state, const T *x, const T *r, const T *i,
                                                     const float *A, T *h, GlrDims d, int blocks) {
@@ -563,8 +565,9 @@ __global__ void __launch_bounds__(128) k_glr_decode(float *state, const T *x, co
 
 // The reverse scan: c_t = a_t g_t with g_t = dh_t + c_{t+1}, that is c_t = a_t c_{t+1} + a_t dh_t, over
 // tiles from the sequence's end.  Of the gates only the decay is needed before the exchange; it is kept,
-// and the rest is formed when g is known.  Long-context bf16 batch (b = 4, L = 16384, D = 1536): 371 us for
-// 1.61 GB, 4.3 TB/s, 66 % of the measured copy bandwidth; issue slots 53 % busy, as in the forward scan.
+// and the rest is formed when g is known.  Long-context bf16 batch (b = 4, L = 16384, D = 1536): 380 to 392 us a call, by
+// box, for 1.61 GB, 4.2 TB/s, 64 % of the measured copy bandwidth (370 us in a graph); issue slots 53 % busy, as in the
+// forward scan.
 template <typename T, int CW, bool kCluster, int kW, int kT>
 __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
     k_glr_backward(const T *x, const T *r, const T *i, const float *A, const float *init, const T *h, const T *dh,
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(kW * 32, BackwardShape<T>::kResident)
   const Place p = place<kCluster>(d.D, blocks);
   const f2 Ac = load_n(A + p.c, p.n);
   const int64_t step = (int64_t)kTile * p.ranks, tiles = (d.L + step - 1) / step;
-  // this warp's tokens are t .. t + 7; those below 0 lie before the sequence
+  // this warp's tokens are t .. t + kT - 1; those below 0 lie before the sequence
   int64_t t = d.L - kT - (p.rank * kTile + p.warp * kT);
   Rows<T, CW, kT> rows[5];  // r, dh, i, x, h_{t-1}
   const int64_t at = p.b * d.L * d.row, o = p.b * d.L * d.D;

@@ -209,7 +209,7 @@ __device__ __forceinline__ float2 unit_sums(float a, float b, int tpr, f2 *sh) {
 
 // Bound by memory, with the loads of about 10 rows an SM in flight: residual norm of 4096 x 2560 (bf16 beside an fp32
 // stream, 126 MB) 21.6 us, 5.8 TB/s, 89 % of the measured copy bandwidth; gated norm of 4096 x 5120 (fp32 y, 168 MB)
-// 32.1 us, 5.2 TB/s, 80 %.
+// 33.0 us, 5.1 TB/s, 78 %.
 template <Mode M, typename TX, typename TR, int VEC, int NV>
 __global__ void __launch_bounds__(row_threads(NV *VEC))
     k_norm_rows(const TX *x, const float *scale, const TR *wide, const float *w, float eps, TR *wide_out, TX *out,
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(row_threads(NV *VEC))
   store_runs<TX, VEC, NV>(out + row * d.D + c0, at, on, v);
 }
 
-// Gradients of rows too long for registers.  A CTA takes rows blockIdx.x, + gridDim.x, ...; a column belongs to one thread of it, which adds the
-// row's terms to the CTA's partial sums.
+// Gradients of rows too long for registers.  A CTA takes rows blockIdx.x, + gridDim.x, ...; a column belongs to one thread
+// of it, which adds the row's terms to the CTA's partial sums.
 //   kResidual: wide = s, dwide = dresidual_out, x for dscale; writes dx, dwide_out = dresidual
 //   gated:     wide = y, x = z;                                writes dx = dz, dwide_out = dy
 template <Mode M, typename TX, typename TR>
@@ -347,8 +347,9 @@ __global__ void __launch_bounds__(kThreads)
 // after its two sums are known, rather than held in registers.  VEC = 1 (arrays without 16-byte alignment) loads
 // directly.
 // Gated norm of 4096 x 5120 (bf16 beside fp32 y, 294 MB): 66 us with the sum of the partial rows, 4.4 TB/s, 68 % of the
-// measured copy bandwidth; residual norm of 65536 x 768 (906 MB) 199 us, 4.6 TB/s, 70 %.  Bound by each row's own chain
-// (ring, sums, ring, stores) on the 24 warps an SM that the sums' registers leave: issue slots 40 % busy.
+// measured copy bandwidth; residual norm of 65536 x 768 (906 MB) 200 us, 4.5 TB/s, 69 %.  Bound first by reads of shared
+// memory (the ring twice, the weights again for every row: the most frequent stall), then by each row's own chain (ring,
+// sums, ring, stores) on the 24 warps an SM that the sums' registers leave: issue slots 42 % busy.
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
                "l"(src)

@@ -473,7 +473,8 @@ def wait_selftest(workspace, limit_ns: int = 1_000_000, expire: bool = True, str
 
 
 # The calls below are short next to a decode step's host work: the checks first compare what
-# holds for every good call, and _check only words the refusal.
+# holds for every good call, and _check only words the refusal.  Like all calls here they are
+# outside torch's autograd: the gradients are calls of their own.
 
 def _cuda(t: torch.Tensor, name: str) -> int:
     """The tensor's CUDA device index."""

@@ -5,6 +5,7 @@ import re
 import subprocess
 from types import SimpleNamespace
 
+import numpy as np
 import pytest
 import torch
 
@@ -88,3 +89,44 @@ def test_kernels_that_start_early_promise_nothing_of_their_memory():
                 assert "__restrict__" not in head, early[-1]
     assert sorted(early) == ["k_glr_backward", "k_glr_decode", "k_glr_prefill", "k_norm_backward_rows", "k_norm_rows",
                              "k_row_sums"]
+
+
+def test_the_polynomial_of_the_decay():
+    """1 - exp(f) over |f| <= ln 2 / 2, from the coefficients in the kernel's source: as close as its comment says; and
+    the decay a and 1 - a that the fp32 steps around it make, each within a few roundings of its own size."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "selective_state_space_10_b200", "csrc")
+    with open(os.path.join(csrc, "glr.cu")) as f:
+        text = f.read()
+    body = text[text.index("void decay("):]
+    numbers = [float(v) for v in re.findall(r"both\((-?[0-9.e-]+)f\)", body[:body.index("\n}")])]
+    magic, back, ln2 = numbers[:3]
+    coefficients = numbers[3:9]
+    assert (magic, back) == (12582912.0, -12582912.0) and coefficients[4:] == [-0.5, -1.0]
+    f32 = np.float32
+
+    def fma(a, b, c):  # of fp32 values: the product is exact in fp64
+        return (np.float64(a) * np.float64(b) + np.float64(c)).astype(f32)
+
+    f = np.linspace(-0.5, 0.5, 200001) * np.log(2)
+    f = f[np.abs(f) > 1e-8]
+    p = np.zeros_like(f)
+    for k in coefficients:
+        p = p * f + np.float64(f32(k))
+    assert np.abs(p * f / -np.expm1(f) - 1).max() < 1.85e-8
+    L = -np.concatenate([np.geomspace(1e-30, 86.9, 200001), np.linspace(0, 3, 100001)[1:]]).astype(f32)
+    t = fma(L, f32(1.4426950408889634), f32(magic))
+    n = t + f32(back)
+    f = fma(n, f32(ln2), L)
+    p = np.full_like(f, f32(coefficients[0]))
+    for k in coefficients[1:]:
+        p = fma(p, f, f32(k))
+    p = p * f
+    two_n = np.exp2(n.astype(np.float64)).astype(f32)
+    v, a = fma(two_n, p, fma(two_n, f32(-1), f32(1))), two_n * fma(p, f32(-1), f32(1))
+    true = np.exp(L.astype(np.float64)), -np.expm1(L.astype(np.float64))
+    U = 2.0 ** -24
+    # f: its sum is rounded once, within U / 2 of ln 2 / 2 at n != 0, and the constant is U / 20 of |L| off; p adds four
+    # roundings that shrink with f, its own and the last product's; then 1 - p and 2^n
+    assert (np.abs(a / true[0] - 1) <= U * (4 + np.abs(L) / 16)).all()
+    # 1 - a: the same, but 2^n p may cancel half of 1 - 2^n, which is exact or rounded to 1
+    assert (np.abs(v / true[1] - 1) <= U * 8).all()
