@@ -375,7 +375,8 @@ SSD_API ssd_status ssd_decode_window_flush(const ssd_dims *dims, ssd_dtype dtype
  * CTAs that share a long sequence take its tiles in turn and wait for one another's part of
  * each round of tiles for at most 2 s.  Where a wait expires, what would have depended on it
  * is NaN: that CTA's tokens of the round, and all tokens of the sequence's 64 channels in every
- * later round (in the order of the scan), with the state after them.  What is finite is right.
+ * later round (in the order of the scan), with the state after them and, of the gradient, those
+ * channels of dA.  What is finite is right.
  */
 typedef struct {
   int64_t batch;       /* >= 0                                                           */
